@@ -165,6 +165,110 @@ q4g_status q4g_flash_decode_linear_i8(const uint16_t* q, int32_t n_q, int32_t n_
                                       const float* v_scales, int64_t len, uint16_t* out, void* workspace,
                                       size_t workspace_bytes, q4g_stream_t stream);
 
+/* Writing K/V rows into an int8 cache as they are produced, and reading them back
+ * (the kv_int8 row format of q4g_config and of the _i8 entry points above): per
+ * row of head_dim values one fp32 scale = amax / 127 and int8 codes
+ * clamp(rint(x / scale), -127, 127) (IEEE fp32 divisions, as a decode step
+ * quantises its rows); read back, a value is fp16(code * scale). A zero row has
+ * scale 0 and codes 0. A NaN value becomes code 0; a row with an infinite value
+ * has an infinite scale and reads back as NaN.
+ *
+ * k and v: fp16 rows [n_rows][n_kv][head_dim], consecutive rows row_stride
+ * elements apart (row_stride >= n_kv * head_dim, a multiple of 8, so that the k
+ * or v columns of a wider projection can be passed as they are).
+ *
+ * _linear: cache [capacity][n_kv][head_dim] with scales [capacity][n_kv], as
+ *   q4g_flash_decode_linear_i8 and q4g_flash_decode_shared_i8 read it. Row t goes
+ *   to cache row slot0 + t (slots == NULL; Q4G_ERANGE unless slot0 + n_rows <=
+ *   capacity), or to cache row slots[t] (device int64 [n_rows], slot0 must be 0):
+ *   a slot outside [0, capacity) skips the row on a write and gives a row of
+ *   zeros on a read. A write that names one slot twice leaves that cache row
+ *   unspecified; reads may repeat slots.
+ * _ring: cache [n_kv][ring][head_dim] with scales [n_kv][ring], as
+ *   q4g_flash_decode_ring_i8 reads it (one layer's ring region of a kv_int8
+ *   cache, see q4g_cache_view). Row t belongs to position pos0 + t and slot
+ *   (pos0 + t) mod ring. Of a write of more than `ring` rows the last `ring` are
+ *   kept; a read takes at most `ring` rows (Q4G_ERANGE). pos0 is any non-negative
+ *   int64 with pos0 + n_rows below 2^63.
+ *
+ * Cache rows that no input row names are left as they were. head_dim must be 256
+ * or 512, 1 <= capacity, ring <= 2^30, n_rows * n_kv <= 2^30 (n_rows = 0 does
+ * nothing). Codes and fp16 rows 16-byte aligned, scales 4-byte, slots 8-byte.
+ * Asynchronous, no scratch memory, one launch. */
+q4g_status q4g_kv_write_linear_i8(const uint16_t* k, const uint16_t* v, int64_t n_rows, int64_t row_stride,
+                                  int32_t n_kv, int32_t head_dim, const int64_t* slots, int64_t slot0,
+                                  int64_t capacity, int8_t* k_codes, float* k_scales, int8_t* v_codes,
+                                  float* v_scales, q4g_stream_t stream);
+q4g_status q4g_kv_write_ring_i8(const uint16_t* k, const uint16_t* v, int64_t n_rows, int64_t row_stride,
+                                int32_t n_kv, int32_t head_dim, int64_t pos0, int64_t ring, int8_t* k_codes,
+                                float* k_scales, int8_t* v_codes, float* v_scales, q4g_stream_t stream);
+q4g_status q4g_kv_read_linear_i8(const int8_t* k_codes, const float* k_scales, const int8_t* v_codes,
+                                 const float* v_scales, int32_t n_kv, int32_t head_dim, const int64_t* slots,
+                                 int64_t slot0, int64_t capacity, int64_t n_rows, uint16_t* k, uint16_t* v,
+                                 int64_t row_stride, q4g_stream_t stream);
+q4g_status q4g_kv_read_ring_i8(const int8_t* k_codes, const float* k_scales, const int8_t* v_codes,
+                               const float* v_scales, int32_t n_kv, int32_t head_dim, int64_t pos0, int64_t ring,
+                               int64_t n_rows, uint16_t* k, uint16_t* v, int64_t row_stride, q4g_stream_t stream);
+
+/* Flash-decode of a batch whose sequences share a prefix (several continuations,
+ * or several drafts, of one prompt): every prefix row is read once for the whole
+ * batch. q [batch][n_q][hd] fp16, one query per sequence; prefix K/V
+ * [prefix_len][n_kv][hd]; each sequence's own rows K/V
+ * [batch][own_capacity][n_kv][hd], of which the first own_len[b] (device int32
+ * [batch], clamped into [0, own_capacity]) are attended, the query's own row
+ * among them. Sequence b's queries attend all prefix rows and its own rows; query
+ * head h uses KV head h / (n_q / n_kv). Scale 1.0, fp32 online softmax, fp16
+ * output [batch][n_q][hd]; a sequence without any row (prefix_len 0, own_len 0)
+ * gives zeros. Own rows from own_len[b] on are never used, whatever they hold.
+ * hd must be 256 or 512; 1 <= batch <= 256, n_q <= 1024, 0 <= prefix_len <= 2^30,
+ * 0 <= own_capacity <= 2^24, batch * own_capacity <= 2^30 (k_prefix and v_prefix
+ * may be NULL if prefix_len is 0; k_own, v_own and own_len if own_capacity is 0).
+ * workspace: device buffer of q4g_flash_decode_shared_workspace_bytes(batch, n_q,
+ * n_kv, hd) bytes, 256-byte aligned, used as scratch by this call (calls that
+ * share a workspace must not overlap on the GPU). Every wait inside the kernel is
+ * limited in time; one that gives up sets the error word that q4g_model_check
+ * reports. */
+size_t q4g_flash_decode_shared_workspace_bytes(int32_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
+q4g_status q4g_flash_decode_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim,
+                                   const uint16_t* k_prefix, const uint16_t* v_prefix, int64_t prefix_len,
+                                   const uint16_t* k_own, const uint16_t* v_own, int64_t own_capacity,
+                                   const int32_t* own_len, uint16_t* out, void* workspace,
+                                   size_t workspace_bytes, q4g_stream_t stream);
+
+/* The same over int8 rows with one fp32 scale each: prefix scales
+ * [prefix_len][n_kv], own scales [batch][own_capacity][n_kv]. Codes 16-byte
+ * aligned, scales 4-byte aligned. Own rows from own_len[b] on, and their scales,
+ * are never used. Otherwise as above. */
+q4g_status q4g_flash_decode_shared_i8(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_kv,
+                                      int32_t head_dim, const int8_t* k_prefix_codes,
+                                      const float* k_prefix_scales, const int8_t* v_prefix_codes,
+                                      const float* v_prefix_scales, int64_t prefix_len,
+                                      const int8_t* k_own_codes, const float* k_own_scales,
+                                      const int8_t* v_own_codes, const float* v_own_scales, int64_t own_capacity,
+                                      const int32_t* own_len, uint16_t* out, void* workspace,
+                                      size_t workspace_bytes, q4g_stream_t stream);
+
+/* Log probabilities of given tokens, with the entropy and the likeliest
+ * alternatives, from rows of logits (a step's or a verify block's): with m the
+ * row's largest logit, d_i = (logits[r][i] - m) / temperature and S = sum exp(d_i),
+ *   logprob[r]  = d_targets[r] - ln S,   entropy[r] = ln S - sum(exp(d_i) d_i) / S,
+ *   top_ids[r][0..n_top-1] the tokens of the largest logits in falling order (the
+ *   lowest index first on ties) and top_logprobs their log probabilities.
+ * logits: fp32 [rows][vocab], rows row_stride >= vocab elements apart, 4-byte
+ * aligned. targets: device int32 [rows]. A target outside [0, vocab) reads
+ * nothing and gives a NaN logprob. A logit of -inf has probability 0; a row of
+ * nothing else gives -inf log probabilities, entropy 0 and the first n_top
+ * indices. A row with a NaN or +inf logit gives NaN, and unspecified top_ids
+ * inside [0, vocab). targets and logprob may both be NULL, so may entropy, and
+ * top_ids and top_logprobs if n_top is 0 (either may be NULL otherwise, not both).
+ * 0 <= rows <= 2^20, 1 <= vocab <= 2^30, 0 <= n_top <= min(32, vocab), temperature
+ * finite and > 0. fp32 sums; the same bits on every call. Asynchronous, no scratch
+ * memory, one launch. */
+#define Q4G_LOGPROBS_MAX_TOP 32
+q4g_status q4g_token_logprobs(const float* logits, int64_t rows, int64_t vocab, int64_t row_stride,
+                              float temperature, const int32_t* targets, float* logprob, float* entropy,
+                              int32_t n_top, int32_t* top_ids, float* top_logprobs, q4g_stream_t stream);
+
 /* Allocation-free variant of q4g_flash_decode_ring (no counterpart on the pages;
  * an integration convenience). It is for callers that cannot allocate device
  * memory at call time -- for example a program whose device memory belongs to a
@@ -422,6 +526,17 @@ q4g_status q4g_verify_block(q4g_model* m, q4g_cache* c, const int32_t* ids, int3
  * pos0 < 0, pos0 + S > capacity. */
 q4g_status q4g_prefill_chunk(q4g_model* m, q4g_cache* c, const int32_t* ids, int32_t S, int64_t pos0,
                              float* logits, int32_t* argmax, q4g_stream_t stream);
+
+/* Scoring of a chunk: as q4g_prefill_chunk (the rows are written to the cache, the
+ * result is that of S decode steps in order), with the head run for every row and
+ * its softcapped logits handed to q4g_token_logprobs: targets[i] (device int32
+ * [S]) is the token whose log probability row i gives, for a text its next token
+ * ids[i + 1]. Outputs, device: logprob [S], entropy [S], top_ids and top_logprobs
+ * [S][n_top], argmax [S], each NULL if not wanted (at least one is, else
+ * Q4G_EINVAL; targets and logprob go together); temperature and n_top as there. */
+q4g_status q4g_score_chunk(q4g_model* m, q4g_cache* c, const int32_t* ids, const int32_t* targets, int32_t S,
+                           int64_t pos0, float temperature, float* logprob, float* entropy, int32_t n_top,
+                           int32_t* top_ids, float* top_logprobs, int32_t* argmax, q4g_stream_t stream);
 
 #ifdef __cplusplus
 }

@@ -1144,6 +1144,43 @@ extern "C" q4g_status q4g_prefill_chunk(q4g_model* m, q4g_cache* c, const int32_
   return Q4G_OK;
 }
 
+extern "C" q4g_status q4g_score_chunk(q4g_model* m, q4g_cache* c, const int32_t* ids, const int32_t* targets,
+                                      int32_t S, int64_t pos0, float temperature, float* logprob, float* entropy,
+                                      int32_t n_top, int32_t* top_ids, float* top_logprobs, int32_t* argmax,
+                                      q4g_stream_t stream) {
+  if (!m || !c || !ids) return fail(Q4G_EINVAL, "NULL argument");
+  if (S < 1 || S > kPrefillChunk) return fail(Q4G_ERANGE, "S must be 1..%d", kPrefillChunk);
+  if (pos0 < 0 || pos0 > c->capacity - S) return fail(Q4G_ERANGE, "chunk outside [0, capacity)");
+  if (!targets && !entropy && n_top == 0 && !argmax) return fail(Q4G_EINVAL, "no output");
+  const int V = m->cfg.vocab;
+  LogprobParams all;
+  const int bad = make_logprobs(m->logits_buf, S, V, V, temperature, targets, logprob, entropy, n_top, top_ids,
+                                top_logprobs, &all);
+  if (bad) return (q4g_status)bad;
+  // passes of up to 4 rows as in q4g_prefill_chunk, each with the head; the next pass
+  // overwrites the logits after this pass's reduction, in stream order
+  const int kb = std::min(kPrefillBlock, m->cfg.ring - m->cfg.window);
+  const cudaStream_t st = (cudaStream_t)stream;
+  for (int b0 = 0; b0 < S; b0 += kb) {
+    const int n = std::min(kb, S - b0);
+    q4g_status r = run_step(m, c, n, pos0 + b0, ids + b0, nullptr, nullptr, m->logits_buf, m->argmax_buf, st);
+    if (r != Q4G_OK) return r;
+    if (targets || entropy || n_top) {
+      LogprobParams p = all;
+      p.rows = n;
+      if (p.targets) p.targets += b0;
+      if (p.logprob) p.logprob += b0;
+      if (p.entropy) p.entropy += b0;
+      if (p.top_ids) p.top_ids += (size_t)b0 * n_top;
+      if (p.top_logprobs) p.top_logprobs += (size_t)b0 * n_top;
+      CK(launch_logprobs(p, st));
+    }
+    if (argmax)
+      CK(cudaMemcpyAsync(argmax + b0, m->argmax_buf, sizeof(int32_t) * n, cudaMemcpyDeviceToDevice, st));
+  }
+  return Q4G_OK;
+}
+
 extern "C" int32_t q4g_model_profile_read(q4g_model* m, q4g_launch_record* out, int32_t max,
                                           q4g_stream_t stream) {
   if (!m || (max > 0 && !out)) {

@@ -189,6 +189,28 @@ struct StepParams {
 cudaError_t launch_step_init(const StepParams& p, cudaStream_t st);
 
 int device_sm_count();
+// Whether p is device memory (or managed memory) of the current device.
+bool on_current_device(const void* p);
+
+// ------------------------------------------------------- log probabilities ----
+// q4g_token_logprobs after its checks (include/q4g.h has the formulas).
+struct LogprobParams {
+  const float* logits;
+  int64_t row_stride;
+  int32_t rows, vocab;
+  float temperature;
+  const int32_t* targets;  // NULL: no logprob
+  float* logprob;
+  float* entropy;          // NULL: not wanted
+  int32_t n_top;           // 0..32
+  int32_t* top_ids;        // NULL: not wanted
+  float* top_logprobs;     // NULL: not wanted
+};
+// The call's checks: a q4g_status (with its message set), and on Q4G_OK the parameters.
+int make_logprobs(const float* logits, int64_t rows, int64_t vocab, int64_t row_stride, float temperature,
+                  const int32_t* targets, float* logprob, float* entropy, int32_t n_top, int32_t* top_ids,
+                  float* top_logprobs, LogprobParams* out);
+cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t st);
 
 // Sets the message q4g_last_error() returns on this thread.
 void set_last_error(const char* msg);

@@ -134,4 +134,14 @@ cudaError_t launch_step_init(const StepParams& p, cudaStream_t st) {
   return cudaGetLastError();
 }
 
+bool on_current_device(const void* p) {
+  cudaPointerAttributes a;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || cudaPointerGetAttributes(&a, p) != cudaSuccess) {
+    cudaGetLastError();  // the caller reports it
+    return false;
+  }
+  return a.type == cudaMemoryTypeManaged || (a.type == cudaMemoryTypeDevice && a.device == dev);
+}
+
 }  // namespace q4g

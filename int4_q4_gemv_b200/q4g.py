@@ -29,8 +29,12 @@ EXPORTS = [
     "q4g_decode_step", "q4g_decode_step_device_token", "q4g_decode_step_hidden",
     "q4g_decode_step_host", "q4g_verify_block", "q4g_prefill_chunk", "q4g_model_profile_read",
     "q4g_flash_decode_ring_noalloc", "q4g_set_gemv_kernel",
+    "q4g_kv_write_linear_i8", "q4g_kv_write_ring_i8", "q4g_kv_read_linear_i8", "q4g_kv_read_ring_i8",
+    "q4g_flash_decode_shared_workspace_bytes", "q4g_flash_decode_shared", "q4g_flash_decode_shared_i8",
+    "q4g_token_logprobs", "q4g_score_chunk",
 ]
 Q4G_NOALLOC_SCRATCH_BYTES = 1 << 20
+Q4G_LOGPROBS_MAX_TOP = 32
 
 
 class Q4GError(RuntimeError):
@@ -120,6 +124,17 @@ def lib() -> C.CDLL:
             "q4g_model_profile_read": (i32, [vp, C.POINTER(q4g_launch_record), i32, vp]),
             "q4g_flash_decode_ring_noalloc": (C.c_int, [vp, i32, i32, i32, vp, vp, i64, i64, i64, vp, vp]),
             "q4g_set_gemv_kernel": (C.c_int, [i32]),
+            "q4g_kv_write_linear_i8": (C.c_int, [vp, vp, i64, i64, i32, i32, vp, i64, i64, vp, vp, vp, vp, vp]),
+            "q4g_kv_write_ring_i8": (C.c_int, [vp, vp, i64, i64, i32, i32, i64, i64, vp, vp, vp, vp, vp]),
+            "q4g_kv_read_linear_i8": (C.c_int, [vp, vp, vp, vp, i32, i32, vp, i64, i64, i64, vp, vp, i64, vp]),
+            "q4g_kv_read_ring_i8": (C.c_int, [vp, vp, vp, vp, i32, i32, i64, i64, i64, vp, vp, i64, vp]),
+            "q4g_flash_decode_shared_workspace_bytes": (sz, [i32, i32, i32, i32]),
+            "q4g_flash_decode_shared": (C.c_int, [vp, i32, i32, i32, i32, vp, vp, i64, vp, vp, i64, vp, vp, vp, sz,
+                                                  vp]),
+            "q4g_flash_decode_shared_i8": (C.c_int, [vp, i32, i32, i32, i32, vp, vp, vp, vp, i64, vp, vp, vp, vp, i64,
+                                                     vp, vp, vp, sz, vp]),
+            "q4g_token_logprobs": (C.c_int, [vp, i64, i64, i64, f32, vp, vp, vp, i32, vp, vp, vp]),
+            "q4g_score_chunk": (C.c_int, [vp, vp, vp, vp, i32, i64, f32, vp, vp, i32, vp, vp, vp, vp]),
         }
         for name, (res, args) in sig.items():
             fn = getattr(L, name)
@@ -199,6 +214,54 @@ def q4g_flash_decode_ring_noalloc(q, n_q, n_kv, head_dim, k_ring, v_ring, ring, 
           stream)
 
 
+def q4g_kv_write_linear_i8(k, v, n_rows, row_stride, n_kv, head_dim, slots, slot0, capacity, k_codes, k_scales,
+                           v_codes, v_scales, stream):
+    _call("q4g_kv_write_linear_i8", k, v, n_rows, row_stride, n_kv, head_dim, slots, slot0, capacity, k_codes,
+          k_scales, v_codes, v_scales, stream)
+
+
+def q4g_kv_write_ring_i8(k, v, n_rows, row_stride, n_kv, head_dim, pos0, ring, k_codes, k_scales, v_codes, v_scales,
+                         stream):
+    _call("q4g_kv_write_ring_i8", k, v, n_rows, row_stride, n_kv, head_dim, pos0, ring, k_codes, k_scales, v_codes,
+          v_scales, stream)
+
+
+def q4g_kv_read_linear_i8(k_codes, k_scales, v_codes, v_scales, n_kv, head_dim, slots, slot0, capacity, n_rows, k, v,
+                          row_stride, stream):
+    _call("q4g_kv_read_linear_i8", k_codes, k_scales, v_codes, v_scales, n_kv, head_dim, slots, slot0, capacity,
+          n_rows, k, v, row_stride, stream)
+
+
+def q4g_kv_read_ring_i8(k_codes, k_scales, v_codes, v_scales, n_kv, head_dim, pos0, ring, n_rows, k, v, row_stride,
+                        stream):
+    _call("q4g_kv_read_ring_i8", k_codes, k_scales, v_codes, v_scales, n_kv, head_dim, pos0, ring, n_rows, k, v,
+          row_stride, stream)
+
+
+def q4g_flash_decode_shared_workspace_bytes(batch, n_q, n_kv, head_dim) -> int:
+    return int(lib().q4g_flash_decode_shared_workspace_bytes(batch, n_q, n_kv, head_dim))
+
+
+def q4g_flash_decode_shared(q, batch, n_q, n_kv, head_dim, k_prefix, v_prefix, prefix_len, k_own, v_own, own_capacity,
+                            own_len, out, ws, ws_bytes, stream):
+    _call("q4g_flash_decode_shared", q, batch, n_q, n_kv, head_dim, k_prefix, v_prefix, prefix_len, k_own, v_own,
+          own_capacity, own_len, out, ws, ws_bytes, stream)
+
+
+def q4g_flash_decode_shared_i8(q, batch, n_q, n_kv, head_dim, k_prefix_codes, k_prefix_scales, v_prefix_codes,
+                               v_prefix_scales, prefix_len, k_own_codes, k_own_scales, v_own_codes, v_own_scales,
+                               own_capacity, own_len, out, ws, ws_bytes, stream):
+    _call("q4g_flash_decode_shared_i8", q, batch, n_q, n_kv, head_dim, k_prefix_codes, k_prefix_scales,
+          v_prefix_codes, v_prefix_scales, prefix_len, k_own_codes, k_own_scales, v_own_codes, v_own_scales,
+          own_capacity, own_len, out, ws, ws_bytes, stream)
+
+
+def q4g_token_logprobs(logits, rows, vocab, row_stride, temperature, targets, logprob, entropy, n_top, top_ids,
+                       top_logprobs, stream):
+    _call("q4g_token_logprobs", logits, rows, vocab, row_stride, temperature, targets, logprob, entropy, n_top,
+          top_ids, top_logprobs, stream)
+
+
 def q4g_model_create(cfg: q4g_config, weights: q4g_weights) -> int:
     h = C.c_void_p()
     _call("q4g_model_create", C.byref(cfg), C.byref(weights), C.byref(h))
@@ -265,6 +328,12 @@ def q4g_verify_block(model, cache, ids, K, pos0, accepted_count, logits, argmax,
 
 def q4g_prefill_chunk(model, cache, ids, S, pos0, logits, argmax, stream):
     _call("q4g_prefill_chunk", model, cache, ids, S, pos0, logits, argmax, stream)
+
+
+def q4g_score_chunk(model, cache, ids, targets, S, pos0, temperature, logprob, entropy, n_top, top_ids, top_logprobs,
+                    argmax, stream):
+    _call("q4g_score_chunk", model, cache, ids, targets, S, pos0, temperature, logprob, entropy, n_top, top_ids,
+          top_logprobs, argmax, stream)
 
 
 def q4g_model_profile_read(model, stream, max_records: int = 1 << 16):
