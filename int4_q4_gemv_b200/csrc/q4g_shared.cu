@@ -75,10 +75,15 @@ struct alignas(64) SharedMaps {
 };
 
 // ------------------------------------------------------------- the work line ----
+// A unit takes its tiles and kUnitCost places before them: starting one (its queries,
+// the first tile's latency, the partial) costs about as long as kUnitCost tiles.
+constexpr int kUnitCost = 1;
+Q4G_DEV int64_t places(int64_t tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+
 struct Line {
-  int64_t prefix_tiles, total;  // tiles of one prefix unit; of the whole call
-  const int32_t* own_tiles;     // [batch + 1] tiles of one KV head's own rows, summed up
-  int32_t ctas;                 // pieces of the line: no more than tiles, so that none is empty
+  int64_t prefix, total;      // places of one prefix unit; of the whole call
+  const int32_t* own_places;  // [batch + 1] places of one KV head's own rows, summed up
+  int32_t ctas;               // pieces of the line: no more than places, so that none is empty
 };
 
 struct Segment {
@@ -95,15 +100,16 @@ Q4G_DEV int own_len_of(const SharedParams& p, int b) {
   return p.own_cap > 0 ? min(max(p.own_len[b], 0), p.own_cap) : 0;
 }
 
-// The part of [t, end) that lies in the unit of tile t.
-Q4G_DEV Segment segment_at(const SharedParams& p, const Line& w, int64_t t, int64_t end, int cta) {
+// The part of the places [t, end) that lies in the unit of place t; moves t behind it.
+// tiles = 0: nothing but places before the unit's first tile.
+Q4G_DEV Segment next_segment(const SharedParams& p, const Line& w, int64_t& t, int64_t end, int cta) {
   Segment s;
-  const int64_t in_prefix = (int64_t)p.n_kv * p.groups * w.prefix_tiles;
+  const int64_t in_prefix = (int64_t)p.n_kv * p.groups * w.prefix;
   int64_t j, len, n;
   if (t < in_prefix) {
-    const int64_t u = t / w.prefix_tiles;
-    j = t - u * w.prefix_tiles;
-    n = w.prefix_tiles;
+    const int64_t u = t / w.prefix;
+    j = t - u * w.prefix;
+    n = w.prefix;
     len = p.prefix;
     s.own = 0, s.b = 0;
     s.h = (int)(u / p.groups);
@@ -113,15 +119,15 @@ Q4G_DEV Segment segment_at(const SharedParams& p, const Line& w, int64_t t, int6
   } else {
     const int per = p.n_kv * p.own_groups;
     const int64_t x = t - in_prefix;
-    int lo = 0, hi = p.batch - 1;  // the last sequence that starts at or before x and is not empty
+    int lo = 0, hi = p.batch - 1;  // the last sequence that starts at or before x: it is not empty
     while (lo < hi) {
       const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)w.own_tiles[mid] * per <= x) lo = mid;
+      if ((int64_t)w.own_places[mid] * per <= x) lo = mid;
       else hi = mid - 1;
     }
     s.b = lo;
-    n = w.own_tiles[lo + 1] - w.own_tiles[lo];
-    const int64_t y = x - (int64_t)w.own_tiles[lo] * per;
+    n = w.own_places[lo + 1] - w.own_places[lo];
+    const int64_t y = x - (int64_t)w.own_places[lo] * per;
     const int u = (int)(y / n);
     j = y - (int64_t)u * n;
     len = own_len_of(p, lo);
@@ -131,36 +137,38 @@ Q4G_DEV Segment segment_at(const SharedParams& p, const Line& w, int64_t t, int6
     s.n_rows = min(kGroupRows, p.G - s.row0);
     s.slot = (int64_t)lo * per + u + cta;
   }
-  s.tiles = (int32_t)min(n - j, end - t);
-  s.key0 = j * kTileKeys;
+  const int64_t e = min(n, j + end - t);
+  t += e - j;
+  const int64_t first = max(j - kUnitCost, (int64_t)0);
+  s.tiles = (int32_t)max(e - kUnitCost - first, (int64_t)0);
+  s.key0 = first * kTileKeys;
   s.key_end = min(len, s.key0 + (int64_t)s.tiles * kTileKeys);
   return s;
 }
 
-// own_tiles[0..batch] and the totals, by one warp.
-Q4G_DEV void sum_own_tiles(const SharedParams& p, int32_t* own_tiles, int lane) {
+// own_places[0..batch], by one warp.
+Q4G_DEV void sum_own_places(const SharedParams& p, int32_t* own_places, int lane) {
   int base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
-    int v = b < p.batch ? (own_len_of(p, b) + kTileKeys - 1) / kTileKeys : 0;
+    int v = b < p.batch ? (int)places((own_len_of(p, b) + kTileKeys - 1) / kTileKeys) : 0;
     const int mine = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, v, o);
       if (lane >= o) v += u;
     }
-    if (b < p.batch) own_tiles[b] = base + v - mine;
+    if (b < p.batch) own_places[b] = base + v - mine;
     base += __shfl_sync(0xffffffffu, v, 31);
   }
-  if (lane == 0) own_tiles[p.batch] = base;
+  if (lane == 0) own_places[p.batch] = base;
 }
 
-Q4G_DEV Line make_line(const SharedParams& p, const int32_t* own_tiles) {
+Q4G_DEV Line make_line(const SharedParams& p, const int32_t* own_places) {
   Line w;
-  w.prefix_tiles = (p.prefix + kTileKeys - 1) / kTileKeys;
-  w.own_tiles = own_tiles;
-  w.total = (int64_t)p.n_kv * p.groups * w.prefix_tiles +
-            (int64_t)own_tiles[p.batch] * p.n_kv * p.own_groups;
+  w.prefix = places((p.prefix + kTileKeys - 1) / kTileKeys);
+  w.own_places = own_places;
+  w.total = (int64_t)p.n_kv * p.groups * w.prefix + (int64_t)own_places[p.batch] * p.n_kv * p.own_groups;
   w.ctas = (int)min((int64_t)p.ctas, w.total);
   return w;
 }
@@ -188,7 +196,7 @@ struct State {
   float wmax[4][kGroupRows];  // per key quarter: a tile's column maxima; at the end column sums
   float ref[kGroupRows];
   float factor[kGroupRows];
-  int32_t own_tiles[kMaxBatch + 1];
+  int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
   uint64_t full[5], empty[5], code_full[5], code_empty[5];
   uint64_t s_full[2], s_free[2], p_full, pv_done, q_ready, drain;
@@ -243,6 +251,21 @@ Q4G_DEV float ex2(float x) {
   return r;
 }
 
+// Lane i's result is the sum of v[i] over the warp's lanes: halves change places with
+// the lane 16, 8, ... away, 31 shuffles in place of 160.
+Q4G_DEV float lane_sums(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = (lane & o) != 0;
+#pragma unroll
+    for (int i = 0; i < o; ++i) {
+      const float keep = up ? v[i + o] : v[i], give = up ? v[i] : v[i + o];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+    }
+  }
+  return v[0];
+}
+
 // -------------------------------------------------------------------- roles ----
 // Ring items in the order in which the products take them: per segment the K parts of
 // tile 0; then of tile j + 1 and the V parts of tile j in turn; V of the last tile.
@@ -256,7 +279,8 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
   uint32_t it = 0;
   bool ok = true;
   for (int64_t t = line_begin(w, blockIdx.x); t < end && ok;) {
-    const Segment s = segment_at(p, w, t, end, blockIdx.x);
+    const Segment s = next_segment(p, w, t, end, blockIdx.x);
+    if (s.tiles == 0) continue;
     const void* const km = s.own ? &maps.own_k : &maps.k;
     const void* const vm = s.own ? &maps.own_v : &maps.v;
     for (int i = 0; i <= s.tiles && ok; ++i) {
@@ -267,18 +291,21 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
         const int key = (int)(s.key0 + (int64_t)j * kTileKeys);
         for (int c = 0; c < HD / 128; ++c, ++it) {
           const int st = it % NS;
-          if (it >= NS && !(ok = wait(sh, p, &empty[st], (it / NS - 1) & 1))) break;
-          unsigned char* dst = smem + (I8 ? P::kCodes + st * P::kCodeStage : P::kRing + st * P::kStage);
-          mbar_arrive_expect_tx(&full[st], I8 ? P::kCodeStage : P::kStage);
-          for (int half = 0; half < (I8 ? 1 : 2); ++half, dst += P::kSlab) {
-            const int x = c * 128 + half * 64;
-            if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[st]);
-            else tma_load_3d(dst, map, x, s.h, key, &full[st]);
+          if (it >= NS && !(ok = wait_warp(sh, p, &empty[st], (it / NS - 1) & 1))) break;
+          if (elect_one()) {
+            unsigned char* dst = smem + (I8 ? P::kCodes + st * P::kCodeStage : P::kRing + st * P::kStage);
+            mbar_arrive_expect_tx(&full[st], I8 ? P::kCodeStage : P::kStage);
+#pragma unroll
+            for (int half = 0; half < (I8 ? 1 : 2); ++half, dst += P::kSlab) {
+              const int x = c * 128 + half * 64;
+              if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[st]);
+              else tma_load_3d(dst, map, x, s.h, key, &full[st]);
+            }
           }
+          __syncwarp();
         }
       }
     }
-    t += s.tiles;
   }
   // Given up: the copies in flight still write this CTA's shared memory. Each is the last
   // of its stage, so its phase stays.
@@ -295,11 +322,13 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, con
   const int64_t end = line_begin(w, blockIdx.x + 1);
   uint32_t it = 0, tile = 0, seg = 0;
   bool ok = true;
-  for (int64_t t = line_begin(w, blockIdx.x); t < end && ok; ++seg) {
-    const Segment s = segment_at(p, w, t, end, blockIdx.x);
+  for (int64_t t = line_begin(w, blockIdx.x); t < end && ok;) {
+    const Segment s = next_segment(p, w, t, end, blockIdx.x);
+    if (s.tiles == 0) continue;
     const uint32_t n = (s.n_rows + 15) & ~15;
     const uint32_t id_s = tc_idesc_f16(n, false, false), id_o = tc_idesc_f16(n, true, true);
     if (!(ok = wait_warp(sh, p, &sh.q_ready, seg & 1))) break;
+    ++seg;
     for (int i = 0; i <= s.tiles && ok; ++i) {
       if (i < s.tiles) {  // S^T of tile i
         const uint32_t g = tile + i, buf = g & 1;
@@ -308,7 +337,7 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, con
           const int st = it % NS;
           if (!(ok = wait_warp(sh, p, &sh.full[st], (it / NS) & 1))) break;
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t a = base + P::kRing + st * P::kStage, q = base + P::kQ + 2 * c * P::kQSlab;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -339,7 +368,7 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, con
             __syncwarp();
           }
           tc_fence_after();
-          if (lane == 0) {
+          if (elect_one()) {
             const uint32_t a = base + P::kRing + st * P::kStage, b = base + P::kP;
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -353,10 +382,10 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, con
       }
     }
     tile += s.tiles;
-    t += s.tiles;
   }
   if (!ok) {  // given up: products in flight still use shared and tensor memory
-    if (lane == 0) {
+    __syncwarp();
+    if (elect_one()) {
       tc_commit(&sh.drain);
       mbar_wait_bounded(&sh.drain, 0, p.wait_ns);
     }
@@ -378,7 +407,8 @@ Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, State& sh, cons
   constexpr int NS = P::kStages, NC = P::kCodeStages, C = HD / 128;
   const int tid = threadIdx.x - 32 * (4 + kSoftmaxWarps), lane = tid & 31;
   const int64_t end = line_begin(w, blockIdx.x + 1);
-  const int64_t items = 2 * C * (end - line_begin(w, blockIdx.x));
+  int64_t items = 0;
+  for (int64_t t = line_begin(w, blockIdx.x); t < end;) items += 2 * C * next_segment(p, w, t, end, blockIdx.x).tiles;
   for (int64_t it = 0; it < items; ++it) {
     const int cs = (int)(it % NC), st = (int)(it % NS);
     if (!wait_warp(sh, p, &sh.code_full[cs], (it / NC) & 1)) return;
@@ -421,18 +451,28 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
   // the barriers among these warps have no limit of their own
   bool ok = true;
   for (int64_t t = line_begin(w, blockIdx.x); t < end;) {
-    const Segment s = segment_at(p, w, t, end, blockIdx.x);
+    const Segment s = next_segment(p, w, t, end, blockIdx.x);
+    if (s.tiles == 0) continue;
     const int n = (s.n_rows + 15) & ~15;
-    // the unit's query rows, zeros behind them
-    for (int x = tid; x < n * (HD / 8); x += kSoftmaxThreads) {
-      const int r = x / (HD / 8), ch = x % (HD / 8);
-      uint4 v = make_uint4(0, 0, 0, 0);
-      if (r < s.n_rows) {
-        const int rr = s.row0 + r;
+    // the unit's query rows, zeros behind them; eight loads of a thread in flight
+    constexpr int kRowsAtOnce = kSoftmaxThreads / (HD / 8);
+    const int ch = tid % (HD / 8);
+    const __half* const q_head = p.q + (int64_t)s.h * p.G * HD + ch * 8;
+    unsigned char* const q_dst = smem + P::kQ + (ch >> 3) * P::kQSlab;
+    for (int r0 = tid / (HD / 8); r0 < n; r0 += 8 * kRowsAtOnce) {
+      uint4 v[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i * kRowsAtOnce, rr = s.row0 + r;
         const int b = s.own ? s.b : rr / p.G, g = s.own ? rr : rr % p.G;
-        v = __ldg(reinterpret_cast<const uint4*>(p.q + ((int64_t)b * p.n_q + s.h * p.G + g) * HD + ch * 8));
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (r < s.n_rows) v[i] = __ldg(reinterpret_cast<const uint4*>(q_head + ((int64_t)b * p.n_q + g) * HD));
       }
-      *reinterpret_cast<uint4*>(smem + P::kQ + (ch >> 3) * P::kQSlab + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) = v;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int r = r0 + i * kRowsAtOnce;
+        if (r < n) *reinterpret_cast<uint4*>(q_dst + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) = v[i];
+      }
     }
     fence_async_smem();
     __syncwarp();
@@ -539,11 +579,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
     float* const ml = (s.own ? p.own_ml : p.ml) + s.slot * (s.own ? p.own_rows : p.rows) * 2;
     float* const acc = (s.own ? p.own_acc : p.acc) + s.slot * (s.own ? p.own_rows : p.rows) * HD;
     if (c0 < n) {
-#pragma unroll
-      for (int i = 0; i < 32; ++i) {
-        const float sum = warp_sum(l[i]);
-        if (lane == 0) sh.wmax[quarter][c0 + i] = sum;
-      }
+      sh.wmax[quarter][c0 + lane] = lane_sums(l, lane);
 #pragma unroll 1
       for (int c = 0; c < C; ++c) {
         float o[32];
@@ -560,7 +596,6 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
       ml[2 * tid] = sh.ref[tid];
       ml[2 * tid + 1] = sh.wmax[0][tid] + sh.wmax[1][tid] + sh.wmax[2][tid] + sh.wmax[3][tid];
     }
-    t += s.tiles;
   }
 }
 
@@ -572,7 +607,7 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   State& sh = *reinterpret_cast<State*>(smem + P::kState);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (warp == 0) {
-    sum_own_tiles(p, sh.own_tiles, lane);
+    sum_own_places(p, sh.own_places, lane);
   } else if (warp == 1) {
     tmem_alloc(&sh.tmem, 512);
   } else if (warp == 2 && lane == 0) {
@@ -597,10 +632,9 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Line w = make_line(p, sh.own_tiles);
+  const Line w = make_line(p, sh.own_places);
   if (warp == 0) {
-    if (lane == 0) produce<HD, I8>(p, maps, smem, sh, w);
-    __syncwarp();
+    produce<HD, I8>(p, maps, smem, sh, w);
   } else if (warp == 1) {
     multiply<HD, I8>(p, smem, sh, w);
   } else if (warp >= 4 && warp < 4 + kSoftmaxWarps) {
@@ -618,81 +652,102 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
 
 // ------------------------------------------------------------------ the join ----
 constexpr int kJoinThreads = 256;
-constexpr int kJoinCols = 128;                              // output columns per CTA
-constexpr int kJoinLanes = kJoinCols / 4;                   // threads across them
-constexpr int kJoinParts = kJoinThreads / kJoinLanes;       // threads down the partials
+constexpr int kJoinCols = 128;                          // output columns per CTA
+constexpr int kJoinLanes = kJoinCols / 4;               // threads across them: a warp
+constexpr int kJoinParts = kJoinThreads / kJoinLanes;   // threads down the partials: the warps
+constexpr int kJoinMax = 2 * 256;                       // partials of a row: CTAs of its two units
 
 // out[row] = sum_i 2^(ref_i - R) O_i / sum_i 2^(ref_i - R) l_i over the row's partials,
-// R the largest reference; in a fixed order. Grid: query rows, columns / 128.
+// R the largest reference; in a fixed order. Grid: query rows, columns / 128. The weights
+// are made once, one thread a partial, so that the loads of O depend on nothing.
 template <int HD>
 __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p) {
-  __shared__ int32_t own_tiles[kMaxBatch + 1];
-  __shared__ float red[kJoinThreads / 32];
+  __shared__ int32_t own_places[kMaxBatch + 1];
+  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ float weight[kJoinMax];
   __shared__ float4 part[kJoinParts][kJoinLanes];
-  __shared__ float part_l[kJoinParts];
   pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) sum_own_tiles(p, own_tiles, lane);
+  if (warp == 0) sum_own_places(p, own_places, lane);
   __syncthreads();
-  const Line w = make_line(p, own_tiles);
+  const Line w = make_line(p, own_places);
   const int b = blockIdx.x / p.n_q, hq = blockIdx.x % p.n_q, h = hq / p.G, g = hq % p.G;
   __half* const out = p.out + (int64_t)blockIdx.x * HD + blockIdx.y * kJoinCols;
   // the partials of the row: slots [s0, s0 + n0) of the prefix, [s1, s1 + n1) of its own rows
   int64_t s0 = 0, s1 = 0;
   int n0 = 0, n1 = 0, r0 = 0, r1 = g % kGroupRows;
-  if (w.prefix_tiles > 0) {
+  if (w.prefix > 0) {
     const int rr = b * p.G + g;
-    const int64_t u = (int64_t)h * p.groups + rr / kGroupRows, t = u * w.prefix_tiles;
-    const int c = line_cta(w, t);
+    const int64_t u = (int64_t)h * p.groups + rr / kGroupRows, t = u * w.prefix;
+    const int c = line_cta(w, t + kUnitCost);
     r0 = rr % kGroupRows;
     s0 = u + c;
-    n0 = line_cta(w, t + w.prefix_tiles - 1) - c + 1;
+    n0 = line_cta(w, t + w.prefix - 1) - c + 1;
   }
-  const int tiles = own_tiles[b + 1] - own_tiles[b];
-  if (tiles > 0) {
+  const int own = own_places[b + 1] - own_places[b];
+  if (own > 0) {
     const int per = p.n_kv * p.own_groups, u = h * p.own_groups + g / kGroupRows;
-    const int64_t t = (int64_t)p.n_kv * p.groups * w.prefix_tiles + (int64_t)own_tiles[b] * per + (int64_t)u * tiles;
-    const int c = line_cta(w, t);
+    const int64_t t = (int64_t)p.n_kv * p.groups * w.prefix + (int64_t)own_places[b] * per + (int64_t)u * own;
+    const int c = line_cta(w, t + kUnitCost);
     s1 = (int64_t)b * per + u + c;
-    n1 = line_cta(w, t + tiles - 1) - c + 1;
+    n1 = line_cta(w, t + own - 1) - c + 1;
   }
   const int n = n0 + n1;
-  auto ml_at = [&](int i) {
-    return i < n0 ? p.ml + ((s0 + i) * p.rows + r0) * 2 : p.own_ml + ((s1 + i - n0) * p.own_rows + r1) * 2;
-  };
-  auto acc_at = [&](int i) {
-    return i < n0 ? p.acc + ((s0 + i) * p.rows + r0) * HD : p.own_acc + ((s1 + i - n0) * p.own_rows + r1) * HD;
-  };
+  // references, sums and weights, one or two partials a thread (n <= 2 * CTAs <= kJoinMax)
+  const float* const ml0 = p.ml + (s0 * p.rows + r0) * 2;
+  const float* const ml1 = p.own_ml + (s1 * p.own_rows + r1) * 2;
+  float2 ml[kJoinMax / kJoinThreads];
   float R = -INFINITY;
-  for (int i = tid; i < n; i += kJoinThreads) R = fmaxf(R, ml_at(i)[0]);
+#pragma unroll
+  for (int k = 0; k < kJoinMax / kJoinThreads; ++k) {
+    const int i = tid + k * kJoinThreads;
+    ml[k] = make_float2(-INFINITY, 0.f);
+    if (i < n)
+      ml[k] = *reinterpret_cast<const float2*>(i < n0 ? ml0 + (int64_t)i * p.rows * 2
+                                                      : ml1 + (int64_t)(i - n0) * p.own_rows * 2);
+    R = fmaxf(R, ml[k].x);
+  }
   R = warp_max(R);
-  if (lane == 0) red[warp] = R;
+  if (lane == 0) red[0][warp] = R;
   __syncthreads();
 #pragma unroll
-  for (int i = 0; i < kJoinThreads / 32; ++i) R = fmaxf(R, red[i]);
-  const int col = tid % kJoinLanes, dn = tid / kJoinLanes;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i = 0; i < kJoinThreads / 32; ++i) R = fmaxf(R, red[0][i]);
   float l = 0.f;
-#pragma unroll 4
-  for (int i = dn; i < n; i += kJoinParts) {
-    const float2 ml = *reinterpret_cast<const float2*>(ml_at(i));
-    const float4 a = *reinterpret_cast<const float4*>(acc_at(i) + blockIdx.y * kJoinCols + col * 4);
-    const float f = ex2(ml.x - R);
-    l += f * ml.y;
+#pragma unroll
+  for (int k = 0; k < kJoinMax / kJoinThreads; ++k) {
+    const int i = tid + k * kJoinThreads;
+    if (i < n) {
+      const float f = ex2(ml[k].x - R);
+      weight[i] = f;
+      l += f * ml[k].y;
+    }
+  }
+  l = warp_sum(l);
+  if (lane == 0) red[1][warp] = l;
+  __syncthreads();
+  const float* const acc0 = p.acc + (s0 * p.rows + r0) * HD + blockIdx.y * kJoinCols + lane * 4;
+  const float* const acc1 = p.own_acc + (s1 * p.own_rows + r1) * HD + blockIdx.y * kJoinCols + lane * 4;
+  const int64_t step0 = (int64_t)p.rows * HD, step1 = (int64_t)p.own_rows * HD;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int i = warp; i < n; i += kJoinParts) {
+    const float4 a = *reinterpret_cast<const float4*>(i < n0 ? acc0 + i * step0 : acc1 + (i - n0) * step1);
+    const float f = weight[i];
     o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
   }
-  part[dn][col] = o;
-  if (col == 0) part_l[dn] = l;
+  part[warp][lane] = o;
   __syncthreads();
-  if (dn == 0) {
+  if (warp == 0) {
+    l = red[1][0];
+#pragma unroll
     for (int i = 1; i < kJoinParts; ++i) {
-      const float4 a = part[i][col];
-      l += part_l[i];
+      const float4 a = part[i][lane];
+      l += red[1][i];
       o.x += a.x, o.y += a.y, o.z += a.z, o.w += a.w;
     }
     const float inv = n > 0 ? 1.f / l : 0.f;  // no key at all: zeros
     const __half2 lo = __floats2half2_rn(o.x * inv, o.y * inv), hi = __floats2half2_rn(o.z * inv, o.w * inv);
-    *reinterpret_cast<uint2*>(out + col * 4) =
+    *reinterpret_cast<uint2*>(out + lane * 4) =
         make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
   }
 }
@@ -776,7 +831,7 @@ size_t plan_scratch(SharedParams& p, int hd, void* ws) {
   p.own_groups = (p.G + kGroupRows - 1) / kGroupRows;
   p.rows = rows < kGroupRows ? rows : kGroupRows;
   p.own_rows = p.G < kGroupRows ? p.G : kGroupRows;
-  p.ctas = device_sm_count();
+  p.ctas = device_sm_count() < kJoinMax / 2 ? device_sm_count() : kJoinMax / 2;
   const size_t n = ((size_t)p.n_kv * p.groups + p.ctas) * p.rows;
   const size_t n_own = ((size_t)p.batch * p.n_kv * p.own_groups + p.ctas) * p.own_rows;
   size_t off = 0;
