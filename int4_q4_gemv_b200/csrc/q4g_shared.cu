@@ -47,7 +47,7 @@ constexpr int kGroupRows = 64;   // query rows of one unit, at most
 constexpr int kMaxBatch = 256;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kConvertWarps = 4;
+constexpr int kConvertWarps = 8;  // in two groups that take turns at the ring's items
 constexpr float kHeadroom = 8.f;  // a tile may pass the reference by 2^8
 constexpr float kOffset = 7.f;    // probabilities are scaled by 2^7: 2^15 at most
 constexpr float kLog2e = 1.4426950408889634f;
@@ -93,8 +93,12 @@ struct Segment {
   int64_t slot;
 };
 
-Q4G_DEV int64_t line_begin(const Line& w, int c) { return w.total * min(c, w.ctas) / max(w.ctas, 1); }
-Q4G_DEV int line_cta(const Line& w, int64_t t) { return (int)(((t + 1) * w.ctas - 1) / w.total); }
+// Divisions of 64 bits take some hundred instructions: only calls beyond 2^32 pay them.
+Q4G_DEV int64_t quotient(int64_t a, int64_t b) {
+  return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
+}
+Q4G_DEV int64_t line_begin(const Line& w, int c) { return quotient(w.total * min(c, w.ctas), max(w.ctas, 1)); }
+Q4G_DEV int line_cta(const Line& w, int64_t t) { return (int)quotient((t + 1) * w.ctas - 1, w.total); }
 
 Q4G_DEV int own_len_of(const SharedParams& p, int b) {
   return p.own_cap > 0 ? min(max(p.own_len[b], 0), p.own_cap) : 0;
@@ -107,13 +111,13 @@ Q4G_DEV Segment next_segment(const SharedParams& p, const Line& w, int64_t& t, i
   const int64_t in_prefix = (int64_t)p.n_kv * p.groups * w.prefix;
   int64_t j, len, n;
   if (t < in_prefix) {
-    const int64_t u = t / w.prefix;
+    const int64_t u = quotient(t, w.prefix);
     j = t - u * w.prefix;
     n = w.prefix;
     len = p.prefix;
     s.own = 0, s.b = 0;
-    s.h = (int)(u / p.groups);
-    s.row0 = (int)(u % p.groups) * kGroupRows;
+    s.h = (int)quotient(u, p.groups);
+    s.row0 = (int)(u - (int64_t)s.h * p.groups) * kGroupRows;
     s.n_rows = min(kGroupRows, p.batch * p.G - s.row0);
     s.slot = u + cta;
   } else {
@@ -128,7 +132,7 @@ Q4G_DEV Segment next_segment(const SharedParams& p, const Line& w, int64_t& t, i
     s.b = lo;
     n = w.own_places[lo + 1] - w.own_places[lo];
     const int64_t y = x - (int64_t)w.own_places[lo] * per;
-    const int u = (int)(y / n);
+    const int u = (int)quotient(y, n);
     j = y - (int64_t)u * n;
     len = own_len_of(p, lo);
     s.own = 1;
@@ -179,7 +183,7 @@ Q4G_DEV Line make_line(const SharedParams& p, const int32_t* own_places) {
 template <int HD, bool I8>
 struct Plan {
   static constexpr int kStages = I8 ? 3 : (HD == 512 ? 4 : 5);
-  static constexpr int kCodeStages = I8 ? (HD == 512 ? 3 : 5) : 0;
+  static constexpr int kCodeStages = I8 ? (HD == 512 ? 2 : 4) : 0;
   static constexpr int kThreads = 32 * (4 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
   static constexpr int kSlab = kTileKeys * 128;            // bytes of a 64-column slab
   static constexpr int kStage = 2 * kSlab;
@@ -187,7 +191,8 @@ struct Plan {
   static constexpr int kQSlab = kGroupRows * 128;
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + HD / 64 * kQSlab;
-  static constexpr int kRing = kP + kTileKeys * 128;
+  static constexpr int kPBytes = kTileKeys * 128;            // P^T of a tile; two of them
+  static constexpr int kRing = kP + 2 * kPBytes;
   static constexpr int kCodes = kRing + kStages * kStage;
   static constexpr int kState = kCodes + kCodeStages * kCodeStage;
 };
@@ -199,7 +204,7 @@ struct State {
   int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
   uint64_t full[5], empty[5], code_full[5], code_empty[5];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, q_ready, drain;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
   volatile int abort;
 };
 
@@ -212,6 +217,7 @@ static_assert(smem_bytes<512, false>() <= 232448 && smem_bytes<512, true>() <= 2
               "227 KB of shared memory");
 
 // Bounded wait; a wait that gives up, here or elsewhere in the CTA, ends every role.
+// (mbar_try_wait sleeps; spinning instead took issue slots from the products: +10%.)
 Q4G_DEV bool wait(State& sh, const SharedParams& p, uint64_t* bar, uint32_t phase) {
   if (mbar_try_wait(bar, phase)) return true;
   const uint64_t t0 = global_ns();
@@ -267,8 +273,10 @@ Q4G_DEV float lane_sums(float (&v)[32], int lane) {
 }
 
 // -------------------------------------------------------------------- roles ----
-// Ring items in the order in which the products take them: per segment the K parts of
-// tile 0; then of tile j + 1 and the V parts of tile j in turn; V of the last tile.
+// Ring items in the order in which the products take them: per segment, in step i, the
+// K parts of tile i, then the V parts of tile i - 1. One thread.
+// (Asking L2 for the next tile as well, by prefetch copies, was slower at every length:
+// 16 sequences on a 128K prefix 178 us without, 200 us with.)
 template <int HD, bool I8>
 Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned char* smem, State& sh, const Line& w) {
   using P = Plan<HD, I8>;
@@ -276,33 +284,29 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
   uint64_t* const full = I8 ? sh.code_full : sh.full;
   uint64_t* const empty = I8 ? sh.code_empty : sh.empty;
   const int64_t end = line_begin(w, blockIdx.x + 1);
+  uint32_t st = 0, phase = 1;  // the phase bit before a stage's first use: that wait is over at once
   uint32_t it = 0;
   bool ok = true;
   for (int64_t t = line_begin(w, blockIdx.x); t < end && ok;) {
     const Segment s = next_segment(p, w, t, end, blockIdx.x);
     if (s.tiles == 0) continue;
-    const void* const km = s.own ? &maps.own_k : &maps.k;
-    const void* const vm = s.own ? &maps.own_v : &maps.v;
     for (int i = 0; i <= s.tiles && ok; ++i) {
-      for (int part = 0; part < 2 && ok; ++part) {  // K of tile i, then V of tile i - 1
+      for (int part = 0; part < 2 && ok; ++part) {
         const int j = i - part;
         if (j < 0 || j >= s.tiles) continue;
-        const void* const map = part ? vm : km;
-        const int key = (int)(s.key0 + (int64_t)j * kTileKeys);
+        const void* const map = s.own ? (part ? &maps.own_v : &maps.own_k) : (part ? &maps.v : &maps.k);
+        const int key = (int)s.key0 + j * kTileKeys;
         for (int c = 0; c < HD / 128; ++c, ++it) {
-          const int st = it % NS;
-          if (it >= NS && !(ok = wait_warp(sh, p, &empty[st], (it / NS - 1) & 1))) break;
-          if (elect_one()) {
-            unsigned char* dst = smem + (I8 ? P::kCodes + st * P::kCodeStage : P::kRing + st * P::kStage);
-            mbar_arrive_expect_tx(&full[st], I8 ? P::kCodeStage : P::kStage);
+          if (!(ok = wait(sh, p, &empty[st], phase))) break;
+          unsigned char* dst = smem + (I8 ? P::kCodes + st * P::kCodeStage : P::kRing + st * P::kStage);
+          mbar_arrive_expect_tx(&full[st], I8 ? P::kCodeStage : P::kStage);
 #pragma unroll
-            for (int half = 0; half < (I8 ? 1 : 2); ++half, dst += P::kSlab) {
-              const int x = c * 128 + half * 64;
-              if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[st]);
-              else tma_load_3d(dst, map, x, s.h, key, &full[st]);
-            }
+          for (int half = 0; half < (I8 ? 1 : 2); ++half, dst += P::kSlab) {
+            const int x = c * 128 + half * 64;
+            if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[st]);
+            else tma_load_3d(dst, map, x, s.h, key, &full[st]);
           }
-          __syncwarp();
+          if (++st == NS) st = 0, phase ^= 1;
         }
       }
     }
@@ -313,83 +317,83 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
     for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_bounded(&full[k % NS], (k / NS) & 1, p.wait_ns);
 }
 
+// All products, by one thread.
 template <int HD, bool I8>
 Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, const Line& w) {
   using P = Plan<HD, I8>;
   constexpr int NS = P::kStages, C = HD / 128;
-  const int lane = threadIdx.x & 31;
-  const uint32_t base = smem_u32(smem), s_col = sh.tmem, o_col = sh.tmem + 2 * kGroupRows;
+  const uint32_t ring = smem_u32(smem) + P::kRing, q = smem_u32(smem) + P::kQ, pr = smem_u32(smem) + P::kP;
+  const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kGroupRows;
   const int64_t end = line_begin(w, blockIdx.x + 1);
-  uint32_t it = 0, tile = 0, seg = 0;
+  uint32_t st = 0, phase = 0, tile = 0, seg = 0;
   bool ok = true;
   for (int64_t t = line_begin(w, blockIdx.x); t < end && ok;) {
     const Segment s = next_segment(p, w, t, end, blockIdx.x);
     if (s.tiles == 0) continue;
     const uint32_t n = (s.n_rows + 15) & ~15;
     const uint32_t id_s = tc_idesc_f16(n, false, false), id_o = tc_idesc_f16(n, true, true);
-    if (!(ok = wait_warp(sh, p, &sh.q_ready, seg & 1))) break;
+    if (!(ok = wait(sh, p, &sh.q_ready, seg & 1))) break;
     ++seg;
+    // Step i: S^T of tile i, then O^T += V^T P^T of tile i - 1, whose softmax ran while S^T
+    // of tile i was made. (Part by part in turn, with a tile more between the two, was 7%
+    // slower on 16 sequences and a 32K prefix: every part then pays the wait for its load.)
     for (int i = 0; i <= s.tiles && ok; ++i) {
-      if (i < s.tiles) {  // S^T of tile i
-        const uint32_t g = tile + i, buf = g & 1;
-        if (g >= 2 && !(ok = wait_warp(sh, p, &sh.s_free[buf], (g / 2 - 1) & 1))) break;
-        for (int c = 0; c < C; ++c, ++it) {
-          const int st = it % NS;
-          if (!(ok = wait_warp(sh, p, &sh.full[st], (it / NS) & 1))) break;
+      if (i < s.tiles) {
+        const uint32_t g = tile + i, s_at = s_col + (g & 1) * kGroupRows;
+        if (g >= 2 && !(ok = wait(sh, p, &sh.s_free[g & 1], (g / 2 - 1) & 1))) break;
+        for (int c = 0; c < C; ++c) {
+          if (!(ok = wait(sh, p, &sh.full[st], phase))) break;
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t a = base + P::kRing + st * P::kStage, q = base + P::kQ + 2 * c * P::kQSlab;
+          const uint32_t a = ring + st * P::kStage, b = q + 2 * c * P::kQSlab;
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16(s_col + buf * kGroupRows, tc_desc(a + (k >> 2) * P::kSlab + (k & 3) * 32, 0),
-                         tc_desc(q + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
-            tc_commit(&sh.empty[st]);
-            if (c == C - 1) tc_commit(&sh.s_full[buf]);
-          }
-          __syncwarp();
+          for (int k = 0; k < 8; ++k)
+            tc_mma_f16(s_at, tc_desc(a + (k >> 2) * P::kSlab + (k & 3) * 32, 0),
+                       tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
+          tc_commit(&sh.empty[st]);
+          if (++st == NS) st = 0, phase ^= 1;
         }
         if (!ok) break;
+        tc_commit(&sh.s_full[g & 1]);
       }
-      if (i > 0) {  // O^T += V^T P^T of tile i - 1
-        const uint32_t g = tile + i - 1;
-        if (!(ok = wait_warp(sh, p, &sh.p_full, g & 1))) break;
-        // keys of this tile; what lies behind a sequence's own rows may be anything, and
-        // zero times a NaN is not zero
-        const int live = (int)min((int64_t)kTileKeys, s.key_end - s.key0 - (int64_t)(i - 1) * kTileKeys);
-        for (int c = 0; c < C; ++c, ++it) {
-          const int st = it % NS;
-          if (!(ok = wait_warp(sh, p, &sh.full[st], (it / NS) & 1))) break;
-          if (!I8 && s.own && live < kTileKeys) {
-            for (int x = live * 8 + lane; x < kTileKeys * 8; x += 32)
+      if (i > 0) {
+        const uint32_t g = tile + i - 1, pt = pr + (g & 1) * P::kPBytes;
+        if (!(ok = wait(sh, p, &sh.p_full[g & 1], (g / 2) & 1))) break;
+        // the live keys, rounded up to 16
+        const int live = min(kTileKeys, (int)(s.key_end - s.key0) - (i - 1) * kTileKeys);
+        const int steps = (live + 15) >> 4;
+        for (int c = 0; c < C; ++c) {
+          if (!(ok = wait(sh, p, &sh.full[st], phase))) break;
+          if (!I8 && s.own && live < steps * 16) {
+            // what lies behind a sequence's own rows may be anything, and zero times a NaN
+            // is not zero
+            for (int x = live * 8; x < steps * 128; ++x)
               for (int half = 0; half < 2; ++half)
                 *reinterpret_cast<uint4*>(smem + P::kRing + st * P::kStage + half * P::kSlab + x * 16) =
                     make_uint4(0, 0, 0, 0);
             fence_async_smem();
-            __syncwarp();
           }
           tc_fence_after();
-          if (elect_one()) {
-            const uint32_t a = base + P::kRing + st * P::kStage, b = base + P::kP;
+          const uint32_t a = ring + st * P::kStage, o_at = o_col + c * kGroupRows;
+          if (steps == kTileKeys / 16) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
-              tc_mma_f16(o_col + c * kGroupRows, tc_desc(a + k * 2048, P::kSlab), tc_desc(b + k * 2048, 0), id_o,
-                         i > 1 || k > 0);
-            tc_commit(&sh.empty[st]);
-            if (c == C - 1) tc_commit(&sh.pv_done);
+              tc_mma_f16(o_at, tc_desc(a + k * 2048, P::kSlab), tc_desc(pt + k * 2048, 0), id_o, i > 1 || k > 0);
+          } else {
+            for (int k = 0; k < steps; ++k)
+              tc_mma_f16(o_at, tc_desc(a + k * 2048, P::kSlab), tc_desc(pt + k * 2048, 0), id_o, i > 1 || k > 0);
           }
-          __syncwarp();
+          tc_commit(&sh.empty[st]);
+          if (++st == NS) st = 0, phase ^= 1;
         }
+        if (!ok) break;
+        tc_commit(&sh.pv_done[g & 1]);
       }
     }
     tile += s.tiles;
   }
   if (!ok) {  // given up: products in flight still use shared and tensor memory
-    __syncwarp();
-    if (elect_one()) {
-      tc_commit(&sh.drain);
-      mbar_wait_bounded(&sh.drain, 0, p.wait_ns);
-    }
-    __syncwarp();
+    tc_commit(&sh.drain);
+    mbar_wait_bounded(&sh.drain, 0, p.wait_ns);
   }
 }
 
@@ -401,22 +405,24 @@ Q4G_DEV uint32_t widen2(uint32_t u, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
+constexpr int kGroup = kConvertWarps / 2 * 32;
+
 template <int HD>
 Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, State& sh, const Line& w) {
   using P = Plan<HD, true>;
   constexpr int NS = P::kStages, NC = P::kCodeStages, C = HD / 128;
-  const int tid = threadIdx.x - 32 * (4 + kSoftmaxWarps), lane = tid & 31;
+  const int tid = threadIdx.x - 32 * (4 + kSoftmaxWarps), lane = tid & 31, group = tid / kGroup;
   const int64_t end = line_begin(w, blockIdx.x + 1);
-  int64_t items = 0;
+  uint32_t items = 0;
   for (int64_t t = line_begin(w, blockIdx.x); t < end;) items += 2 * C * next_segment(p, w, t, end, blockIdx.x).tiles;
-  for (int64_t it = 0; it < items; ++it) {
-    const int cs = (int)(it % NC), st = (int)(it % NS);
+  for (uint32_t it = group; it < items; it += 2) {
+    const uint32_t cs = it % NC, st = it % NS;
     if (!wait_warp(sh, p, &sh.code_full[cs], (it / NC) & 1)) return;
     if (it >= NS && !wait_warp(sh, p, &sh.empty[st], (it / NS - 1) & 1)) return;
     const unsigned char* const src = smem + P::kCodes + cs * P::kCodeStage;
     unsigned char* const dst = smem + P::kRing + st * P::kStage;
 #pragma unroll 4
-    for (int x = tid; x < kTileKeys * 8; x += 32 * kConvertWarps) {
+    for (int x = tid % kGroup; x < kTileKeys * 8; x += kGroup) {
       const int row = x >> 3, g = x & 7;  // 16 codes: columns 16 g of the row
       uint4 u = *reinterpret_cast<const uint4*>(src + x * 16);
       u.x ^= 0x80808080u, u.y ^= 0x80808080u, u.z ^= 0x80808080u, u.w ^= 0x80808080u;
@@ -454,24 +460,31 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
     const Segment s = next_segment(p, w, t, end, blockIdx.x);
     if (s.tiles == 0) continue;
     const int n = (s.n_rows + 15) & ~15;
-    // the unit's query rows, zeros behind them; eight loads of a thread in flight
+    // the unit's query rows, zeros behind them; eight loads of a thread in flight. CTAs
+    // start at different rows: most of them read the same ones at the same time
     constexpr int kRowsAtOnce = kSoftmaxThreads / (HD / 8);
     const int ch = tid % (HD / 8);
     const __half* const q_head = p.q + (int64_t)s.h * p.G * HD + ch * 8;
     unsigned char* const q_dst = smem + P::kQ + (ch >> 3) * P::kQSlab;
+    const int turn = (blockIdx.x * 4) % n;
+    const float inv_G = 1.0f / p.G;
     for (int r0 = tid / (HD / 8); r0 < n; r0 += 8 * kRowsAtOnce) {
       uint4 v[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i * kRowsAtOnce, rr = s.row0 + r;
-        const int b = s.own ? s.b : rr / p.G, g = s.own ? rr : rr % p.G;
+        const int at = r0 + i * kRowsAtOnce + turn;
+        const int r = at < n ? at : at - n, rr = s.row0 + r;
+        // rr / G: the quotient is off by less than 2^-23 of itself, rr < 2^18 and G <= 1024 put
+        // (rr + 1/2) / G at least 2^-11 from a whole number while it is below 2^18 / G
+        const int b = s.own ? s.b : (int)((rr + 0.5f) * inv_G), g = s.own ? rr : rr - b * p.G;
         v[i] = make_uint4(0, 0, 0, 0);
-        if (r < s.n_rows) v[i] = __ldg(reinterpret_cast<const uint4*>(q_head + ((int64_t)b * p.n_q + g) * HD));
+        if (r < s.n_rows && at - turn < n) v[i] = __ldg(reinterpret_cast<const uint4*>(q_head + ((int64_t)b * p.n_q + g) * HD));
       }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = r0 + i * kRowsAtOnce;
-        if (r < n) *reinterpret_cast<uint4*>(q_dst + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) = v[i];
+        const int at = r0 + i * kRowsAtOnce + turn;
+        const int r = at < n ? at : at - n;
+        if (at - turn < n) *reinterpret_cast<uint4*>(q_dst + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) = v[i];
       }
     }
     fence_async_smem();
@@ -531,7 +544,8 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
         if (j == 0 || raise) sh.ref[tid] = m;
       }
       raise = softmax_any(raise);
-      if (j > 0) ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);  // P and O^T are free
+      if (raise) ok = ok && wait_warp(sh, p, &sh.pv_done[buf ^ 1], ((tile - 1) / 2) & 1);  // O^T is free
+      else if (j >= 2) ok = ok && wait_warp(sh, p, &sh.pv_done[buf], (tile / 2 - 1) & 1);  // this P^T is free
       if (active) {
         if (raise) {
           tc_fence_after();
@@ -551,7 +565,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
 #pragma unroll
           for (int i = 0; i < 32; ++i) l[i] *= sh.factor[c0 + i];
         }
-        unsigned char* const row = smem + P::kP + key * 128;
+        unsigned char* const row = smem + P::kP + buf * P::kPBytes + key * 128;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           uint32_t h[4];
@@ -569,11 +583,11 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full);
+      if (lane == 0) mbar_arrive(&sh.p_full[buf]);
     }
 
     // the segment's partial
-    ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);
+    ok = ok && wait_warp(sh, p, &sh.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1);
     tc_fence_after();
     softmax_sync();  // wmax is free
     float* const ml = (s.own ? p.own_ml : p.ml) + s.slot * (s.own ? p.own_rows : p.rows) * 2;
@@ -612,17 +626,17 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     tmem_alloc(&sh.tmem, 512);
   } else if (warp == 2 && lane == 0) {
     for (int i = 0; i < 5; ++i) {
-      mbar_init(&sh.full[i], I8 ? kConvertWarps : 1);
+      mbar_init(&sh.full[i], I8 ? kConvertWarps / 2 : 1);
       mbar_init(&sh.empty[i], 1);
       mbar_init(&sh.code_full[i], 1);
-      mbar_init(&sh.code_empty[i], kConvertWarps);
+      mbar_init(&sh.code_empty[i], kConvertWarps / 2);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kSoftmaxWarps);
+      mbar_init(&sh.p_full[i], kSoftmaxWarps);
+      mbar_init(&sh.pv_done[i], 1);
     }
-    mbar_init(&sh.p_full, kSoftmaxWarps);
-    mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.q_ready, kSoftmaxWarps);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
@@ -633,14 +647,26 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const Line w = make_line(p, sh.own_places);
-  if (warp == 0) {
-    produce<HD, I8>(p, maps, smem, sh, w);
-  } else if (warp == 1) {
-    multiply<HD, I8>(p, smem, sh, w);
-  } else if (warp >= 4 && warp < 4 + kSoftmaxWarps) {
+  pdl_launch_dependents();  // the join's CTAs take the places that CTAs of this grid leave
+  // With int8 rows 640 threads start with 96 registers each: the softmax warps take 136,
+  // 4 x 32 x (56 + 2 x 136 + 2 x 72) = 472 x 128 of 480 x 128.
+  if (warp < 4) {
+    if constexpr (I8) regs_dec<56>();
+    if (warp == 0) {
+      if (elect_one()) produce<HD, I8>(p, maps, smem, sh, w);
+      __syncwarp();
+    } else if (warp == 1) {
+      if (elect_one()) multiply<HD, I8>(p, smem, sh, w);
+      __syncwarp();
+    }
+  } else if (warp < 4 + kSoftmaxWarps) {
+    if constexpr (I8) regs_inc<136>();
     softmax<HD, I8>(p, smem, sh, w);
-  } else if (warp >= 4 + kSoftmaxWarps) {
-    if constexpr (I8) convert<HD>(p, smem, sh, w);
+  } else {
+    if constexpr (I8) {
+      regs_dec<72>();
+      convert<HD>(p, smem, sh, w);
+    }
   }
   tc_fence_before();
   __syncthreads();
@@ -651,7 +677,7 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ the join ----
-constexpr int kJoinThreads = 256;
+constexpr int kJoinThreads = 512;
 constexpr int kJoinCols = 128;                          // output columns per CTA
 constexpr int kJoinLanes = kJoinCols / 4;               // threads across them: a warp
 constexpr int kJoinParts = kJoinThreads / kJoinLanes;   // threads down the partials: the warps
@@ -666,7 +692,6 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ float weight[kJoinMax];
   __shared__ float4 part[kJoinParts][kJoinLanes];
-  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (warp == 0) sum_own_places(p, own_places, lane);
   __syncthreads();
@@ -693,11 +718,12 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
     n1 = line_cta(w, t + own - 1) - c + 1;
   }
   const int n = n0 + n1;
-  // references, sums and weights, one or two partials a thread (n <= 2 * CTAs <= kJoinMax)
+  // references, sums and weights, one partial a thread (n <= 2 * CTAs <= kJoinMax)
   const float* const ml0 = p.ml + (s0 * p.rows + r0) * 2;
   const float* const ml1 = p.own_ml + (s1 * p.own_rows + r1) * 2;
   float2 ml[kJoinMax / kJoinThreads];
   float R = -INFINITY;
+  pdl_wait();  // all above comes from the call's own arguments
 #pragma unroll
   for (int k = 0; k < kJoinMax / kJoinThreads; ++k) {
     const int i = tid + k * kJoinThreads;
@@ -729,7 +755,7 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
   const float* const acc1 = p.own_acc + (s1 * p.own_rows + r1) * HD + blockIdx.y * kJoinCols + lane * 4;
   const int64_t step0 = (int64_t)p.rows * HD, step1 = (int64_t)p.own_rows * HD;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
+#pragma unroll 10
   for (int i = warp; i < n; i += kJoinParts) {
     const float4 a = *reinterpret_cast<const float4*>(i < n0 ? acc0 + i * step0 : acc1 + (i - n0) * step1);
     const float f = weight[i];

@@ -125,4 +125,15 @@ Q4G_DEV void tma_load_4d(void* dst, const void* map, int x, int y, int z, int w,
       : "memory");
 }
 
+// Registers of the calling warpgroup (four warps from a multiple of four, all of them): a
+// split must add up to no more than the launch's own threads x registers.
+template <int N>
+Q4G_DEV void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+Q4G_DEV void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 }  // namespace q4g
