@@ -18,16 +18,18 @@
 // product, 2^-11 relative as the fp16 output itself; sums and O^T are fp32. With int8
 // rows the reference covers the weight p * scale, not p, so no scale overflows fp16.
 //
-// Work: the (unit, 128-key tile) pairs of the whole call in one line, cut into equal
-// contiguous pieces, one per CTA (one CTA per SM). A unit is a row group of a KV head
-// over the prefix, or a sequence's heads over its own rows; a piece of a unit leaves
-// one partial (reference, sum, O) and a second kernel joins each row's partials. A
-// unit u and a CTA c meet at most once and both only grow along the line, so u + c
-// numbers the partials without any table, on both sides.
+// Work: a unit is a row group of a KV head over the prefix, or a sequence's heads over
+// its own rows. Prefix units are cut into equally many pieces, so that the CTAs that
+// read the same keys for different row groups do so at the same time and share them
+// through L2 (cut as one line over all units they drifted apart, and 16 sequences on a
+// 128K prefix read HBM four times over: 1.08 GB, 167 us). Own units are cut as a line of
+// 128-key tiles over the CTAs, those without a prefix piece first. Every piece leaves one
+// partial (reference, sum, O), and a second kernel joins each row's partials.
 //
-// Bound by HBM up to about 190 rows per key read (a 128-key tile of hd 512 is 256 KB,
-// about 11,000 cycles of an SM's share of HBM, against 3,000 cycles of products for 64
-// rows); by the tensor cores' shared-memory operands above that.
+// Bound by HBM for one row group (a 128-key tile of hd 512 is 256 KB, 5.6 us of an SM's
+// share of HBM; its products take 64 x 68 cycles, 2.2 us: a product with M = 128 reads
+// 4 KB of A from shared memory in 64 cycles, whatever n up to 64); by the products above
+// two row groups.
 #include <cuda.h>
 #include <math.h>
 
@@ -53,16 +55,17 @@ constexpr float kOffset = 7.f;    // probabilities are scaled by 2^7: 2^15 at mo
 constexpr float kLog2e = 1.4426950408889634f;
 
 struct SharedParams {
-  const __half* q;
   const float* ks[2];  // int8 rows: K and V scales, [0] the prefix's, [1] the sequences' own
   const float* vs[2];
-  int64_t prefix;
-  int32_t own_cap;
+  int32_t prefix, own_cap;
   const int32_t* own_len;
   int32_t batch, n_q, n_kv, G;  // G = n_q / n_kv
-  int32_t groups, own_groups;   // row groups of a KV head: over the prefix, over own rows
+  // A prefix unit: up to 64 rows of a KV head, seqs whole sequences of G heads (G <= 64) or
+  // 64 heads of one; groups of them. An own unit: up to 64 heads of a sequence; parts of them.
+  int32_t seqs, parts, heads, groups;
   int32_t rows, own_rows;       // query rows that a partial of either kind holds
   int32_t ctas;
+  int32_t prefix_tiles, pieces, prefix_ctas;  // pieces of a prefix unit; 0: the units as one line
   // partials: (reference, sum) per row, then O per row; the prefix units' slots, then the own units'
   float *ml, *acc, *own_ml, *own_acc;
   __half* out;
@@ -71,91 +74,50 @@ struct SharedParams {
 };
 
 struct alignas(64) SharedMaps {
-  CUtensorMap k, v, own_k, own_v;
+  CUtensorMap k, v, own_k, own_v, q, own_q;
 };
 
-// ------------------------------------------------------------- the work line ----
-// A unit takes its tiles and kUnitCost places before them: starting one (its queries,
-// the first tile's latency, the partial) costs about as long as kUnitCost tiles.
+// ------------------------------------------------------------------ the work ----
+// On a line a unit takes its tiles and kUnitCost places before them: starting one costs
+// about as long as that many tiles. A line of `total` places is cut into `ctas` pieces
+// (no more than places, so that none is empty); a unit u and a piece c meet at most once
+// and only grow along the line, so u + c numbers the partials, on both sides.
 constexpr int kUnitCost = 1;
-Q4G_DEV int64_t places(int64_t tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
+Q4G_DEV int places(int tiles) { return tiles > 0 ? tiles + kUnitCost : 0; }
 
-struct Line {
-  int64_t prefix, total;      // places of one prefix unit; of the whole call
-  const int32_t* own_places;  // [batch + 1] places of one KV head's own rows, summed up
-  int32_t ctas;               // pieces of the line: no more than places, so that none is empty
-};
-
-struct Segment {
-  int own, b, h, row0, n_rows;
-  int64_t key0, key_end;  // keys [key0, key_end) of the unit's rows
-  int32_t tiles;
-  int64_t slot;
-};
-
-// Divisions of 64 bits take some hundred instructions: only calls beyond 2^32 pay them.
+// a / b for a >= 0, b > 0. A CTA's first own segment waits for about ten of these one after
+// the other, and the compiler's take 40 (32 bits) to some hundred (64 bits) instructions:
+// below 2^23 the quotient comes from an fp32 division, off by at most one either way
+// (2 ulp of at most 2^23), and the remainder corrects it.
 Q4G_DEV int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 23) == 0) {
+    const int x = (int)a, y = (int)b, q = (int)__fdividef((float)x, (float)y), rest = x - q * y;
+    return rest < 0 ? q - 1 : rest >= y ? q + 1 : q;
+  }
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
-Q4G_DEV int64_t line_begin(const Line& w, int c) { return quotient(w.total * min(c, w.ctas), max(w.ctas, 1)); }
-Q4G_DEV int line_cta(const Line& w, int64_t t) { return (int)quotient((t + 1) * w.ctas - 1, w.total); }
+Q4G_DEV int64_t cut_begin(int64_t total, int ctas, int c) { return ctas > 0 ? quotient(total * c, ctas) : 0; }
+Q4G_DEV int cut_of(int64_t total, int ctas, int64_t t) { return (int)quotient((t + 1) * ctas - 1, total); }
+
+// The own units' line: places [0, head) go to the CTAs without a prefix piece, the rest
+// to those with one, so that all have about the same work.
+struct Line {
+  const int32_t* own_places;  // [batch + 1] places of one KV head's own rows, summed up
+  int64_t total, head;
+  int32_t head_ctas, tail_ctas;
+};
 
 Q4G_DEV int own_len_of(const SharedParams& p, int b) {
   return p.own_cap > 0 ? min(max(p.own_len[b], 0), p.own_cap) : 0;
 }
 
-// The part of the places [t, end) that lies in the unit of place t; moves t behind it.
-// tiles = 0: nothing but places before the unit's first tile.
-Q4G_DEV Segment next_segment(const SharedParams& p, const Line& w, int64_t& t, int64_t end, int cta) {
-  Segment s;
-  const int64_t in_prefix = (int64_t)p.n_kv * p.groups * w.prefix;
-  int64_t j, len, n;
-  if (t < in_prefix) {
-    const int64_t u = quotient(t, w.prefix);
-    j = t - u * w.prefix;
-    n = w.prefix;
-    len = p.prefix;
-    s.own = 0, s.b = 0;
-    s.h = (int)quotient(u, p.groups);
-    s.row0 = (int)(u - (int64_t)s.h * p.groups) * kGroupRows;
-    s.n_rows = min(kGroupRows, p.batch * p.G - s.row0);
-    s.slot = u + cta;
-  } else {
-    const int per = p.n_kv * p.own_groups;
-    const int64_t x = t - in_prefix;
-    int lo = 0, hi = p.batch - 1;  // the last sequence that starts at or before x: it is not empty
-    while (lo < hi) {
-      const int mid = (lo + hi + 1) >> 1;
-      if ((int64_t)w.own_places[mid] * per <= x) lo = mid;
-      else hi = mid - 1;
-    }
-    s.b = lo;
-    n = w.own_places[lo + 1] - w.own_places[lo];
-    const int64_t y = x - (int64_t)w.own_places[lo] * per;
-    const int u = (int)quotient(y, n);
-    j = y - (int64_t)u * n;
-    len = own_len_of(p, lo);
-    s.own = 1;
-    s.h = u / p.own_groups;
-    s.row0 = (u % p.own_groups) * kGroupRows;
-    s.n_rows = min(kGroupRows, p.G - s.row0);
-    s.slot = (int64_t)lo * per + u + cta;
-  }
-  const int64_t e = min(n, j + end - t);
-  t += e - j;
-  const int64_t first = max(j - kUnitCost, (int64_t)0);
-  s.tiles = (int32_t)max(e - kUnitCost - first, (int64_t)0);
-  s.key0 = first * kTileKeys;
-  s.key_end = min(len, s.key0 + (int64_t)s.tiles * kTileKeys);
-  return s;
-}
-
-// own_places[0..batch], by one warp.
-Q4G_DEV void sum_own_places(const SharedParams& p, int32_t* own_places, int lane) {
+// own_places[0..batch], by one warp; `len`: own_len_of(lane), loaded earlier.
+Q4G_DEV void sum_own_places(const SharedParams& p, int32_t* own_places, int lane, int len) {
   int base = 0;
   for (int b0 = 0; b0 < p.batch; b0 += 32) {
     const int b = b0 + lane;
-    int v = b < p.batch ? (int)places((own_len_of(p, b) + kTileKeys - 1) / kTileKeys) : 0;
+    if (b0 > 0) len = b < p.batch ? own_len_of(p, b) : 0;
+    int v = places((len + kTileKeys - 1) / kTileKeys);
     const int mine = v;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -170,47 +132,160 @@ Q4G_DEV void sum_own_places(const SharedParams& p, int32_t* own_places, int lane
 
 Q4G_DEV Line make_line(const SharedParams& p, const int32_t* own_places) {
   Line w;
-  w.prefix = places((p.prefix + kTileKeys - 1) / kTileKeys);
   w.own_places = own_places;
-  w.total = (int64_t)p.n_kv * p.groups * w.prefix + (int64_t)own_places[p.batch] * p.n_kv * p.own_groups;
-  w.ctas = (int)min((int64_t)p.ctas, w.total);
+  w.total = (int64_t)own_places[p.batch] * p.n_kv * p.parts;
+  const int idle = p.ctas - p.prefix_ctas;
+  const int64_t load = p.pieces > 0 ? (p.prefix_tiles + p.pieces - 1) / p.pieces + kUnitCost : 0;
+  if (idle == 0) w.head = 0;
+  else if (w.total <= idle * load || p.prefix_ctas == 0) w.head = w.total;
+  else w.head = quotient(idle * (p.prefix_ctas * load + w.total), p.ctas);
+  w.head_ctas = (int)min((int64_t)idle, w.head);
+  w.tail_ctas = (int)min((int64_t)p.prefix_ctas, w.total - w.head);
   return w;
 }
+Q4G_DEV int line_piece(const Line& w, int64_t t) {
+  return t < w.head ? cut_of(w.head, w.head_ctas, t) : w.head_ctas + cut_of(w.total - w.head, w.tail_ctas, t - w.head);
+}
+
+struct Segment {
+  int own, b, h, g0, n_rows;  // first sequence and head, query rows
+  int key0, key_end, tiles;   // keys [key0, key_end) of the unit's rows
+  int64_t slot;
+};
+
+// A CTA's segments, its prefix piece (or its part of the prefix line) first: they need no
+// own length, so that the first can start while those are still on their way.
+struct Work {
+  int64_t t, end;
+  int own;
+  Q4G_DEV Work(const SharedParams& p) : own(0) {
+    const int c = blockIdx.x;
+    if (p.pieces > 0) {
+      t = c, end = c < p.prefix_ctas ? c + 1 : c;
+    } else {
+      const int64_t total = (int64_t)p.n_kv * p.groups * places_h(p);
+      t = p.prefix_ctas > 0 ? cut_begin(total, p.prefix_ctas, c) : 0;
+      end = p.prefix_ctas > 0 ? cut_begin(total, p.prefix_ctas, c + 1) : 0;
+    }
+  }
+  static Q4G_DEV int places_h(const SharedParams& p) { return places(p.prefix_tiles); }
+  // The own units follow: from here on next() takes them.
+  Q4G_DEV void start_own(const SharedParams& p, const Line& w) {
+    own = 1;
+    const int c = blockIdx.x, r = c - p.prefix_ctas;
+    t = end = 0;
+    if (r >= 0 && r < w.head_ctas) {
+      t = cut_begin(w.head, w.head_ctas, r), end = cut_begin(w.head, w.head_ctas, r + 1);
+    } else if (r < 0 && c < w.tail_ctas) {
+      t = w.head + cut_begin(w.total - w.head, w.tail_ctas, c);
+      end = w.head + cut_begin(w.total - w.head, w.tail_ctas, c + 1);
+    }
+  }
+  // The next segment of the current kind; false: there is none. A whole warp calls it.
+  Q4G_DEV bool next(const SharedParams& p, const Line& w, Segment& s) {
+    for (;;) {
+      if (t >= end) return false;
+      s.own = own;
+      int first, len;
+      if (!own) {
+        int u;
+        if (p.pieces > 0) {
+          u = (int)quotient(t, p.pieces);
+          const int k = (int)t - u * p.pieces;
+          first = (int)quotient((int64_t)p.prefix_tiles * k, p.pieces);
+          s.tiles = (int)quotient((int64_t)p.prefix_tiles * (k + 1), p.pieces) - first;
+          s.slot = t;
+          t = end;
+        } else {
+          const int n = places_h(p);
+          u = (int)quotient(t, n);
+          s.slot = (int64_t)u + blockIdx.x;
+          advance(t - (int64_t)u * n, n, first, s.tiles);
+        }
+        s.h = (int)quotient(u, p.groups);
+        const int grp = u - s.h * p.groups;
+        s.b = p.parts == 1 ? grp * p.seqs : grp / p.parts;
+        s.g0 = p.parts == 1 ? 0 : grp % p.parts * kGroupRows;
+        s.n_rows = p.parts == 1 ? min(p.seqs, p.batch - s.b) * p.G : min(kGroupRows, p.G - s.g0);
+        len = p.prefix;
+      } else {
+        const int per = p.n_kv * p.parts;
+        int lo = -1;  // the last sequence that starts at or before t: it is not empty
+        for (int b0 = 0; b0 < p.batch; b0 += 32) {
+          const int b = b0 + (threadIdx.x & 31);
+          lo += __popc(__ballot_sync(0xffffffffu, b < p.batch && (int64_t)w.own_places[b] * per <= t));
+        }
+        const int n = w.own_places[lo + 1] - w.own_places[lo];
+        const int64_t y = t - (int64_t)w.own_places[lo] * per;
+        const int u = (int)quotient(y, n);
+        s.slot = (int64_t)lo * per + u + line_piece(w, t);
+        s.b = lo;
+        s.h = p.parts == 1 ? u : u / p.parts;
+        s.g0 = p.parts == 1 ? 0 : u % p.parts * kGroupRows;
+        s.n_rows = min(kGroupRows, p.G - s.g0);
+        len = own_len_of(p, lo);
+        advance(y - (int64_t)u * n, n, first, s.tiles);
+      }
+      if (s.tiles <= 0) continue;
+      s.key0 = first * kTileKeys;
+      s.key_end = min(len, s.key0 + s.tiles * kTileKeys);
+      return true;
+    }
+  }
+  // From place j of a unit of n places: its tiles [first, first + tiles) up to `end`.
+  Q4G_DEV void advance(int64_t j, int n, int& first, int& tiles) {
+    const int64_t e = min((int64_t)n, j + end - t);
+    t += e - j;
+    first = (int)max(j - kUnitCost, (int64_t)0);
+    tiles = (int)e - kUnitCost - first;
+  }
+};
 
 // ------------------------------------------------------------- shared memory ----
-// A ring stage holds 128 keys x 128 columns of K or V in fp16, as two swizzled slabs of
-// 64 columns. int8 rows arrive in a second ring of 16 KB stages and are widened into it.
+// A ring stage holds 128 keys x 128 columns of K or V in fp16, as two swizzled slabs of 64
+// columns (V's two are the M = 128 of one product). int8 rows arrive in a second ring of
+// 16 KB stages and are widened into it. (Single slabs as K's items gave the ring another
+// half stage and let it go earlier, but each item costs the products 50 ns: 3.5 us a tile
+// of 64 rows against 3.0.)
 template <int HD, bool I8>
 struct Plan {
   static constexpr int kStages = I8 ? 3 : (HD == 512 ? 4 : 5);
-  static constexpr int kCodeStages = I8 ? (HD == 512 ? 2 : 4) : 0;
+  static constexpr int kCodeStages = I8 ? (HD == 512 ? 3 : 5) : 0;
   static constexpr int kThreads = 32 * (4 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
-  static constexpr int kSlab = kTileKeys * 128;            // bytes of a 64-column slab
+  static constexpr int kSlab = kTileKeys * 128;  // bytes
   static constexpr int kStage = 2 * kSlab;
   static constexpr int kCodeStage = kTileKeys * 128;
   static constexpr int kQSlab = kGroupRows * 128;
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + HD / 64 * kQSlab;
-  static constexpr int kPBytes = kTileKeys * 128;            // P^T of a tile; two of them
-  static constexpr int kRing = kP + 2 * kPBytes;
+  static constexpr int kRing = kP + kTileKeys * 128;
   static constexpr int kCodes = kRing + kStages * kStage;
   static constexpr int kState = kCodes + kCodeStages * kCodeStage;
 };
 
+constexpr int kQueue = 4;  // segments that the scheduling warp is ahead at most
+
+// Barriers and small arrays of a CTA, apart from the ring's own barriers.
 struct State {
   float wmax[4][kGroupRows];  // per key quarter: a tile's column maxima; at the end column sums
   float ref[kGroupRows];
   float factor[kGroupRows];
+  Segment seg[kQueue];
+  uint64_t seg_full[kQueue], seg_empty[kQueue];
+  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_free, o_free, drain;
   int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
-  uint64_t full[5], empty[5], code_full[5], code_empty[5];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_ready, drain;
   volatile int abort;
+};
+template <int HD, bool I8>
+struct RingState : State {
+  uint64_t full[Plan<HD, I8>::kStages], empty[Plan<HD, I8>::kStages];
+  uint64_t code_full[Plan<HD, I8>::kCodeStages + 1], code_empty[Plan<HD, I8>::kCodeStages + 1];
 };
 
 template <int HD, bool I8>
 constexpr size_t smem_bytes() {
-  return Plan<HD, I8>::kState + sizeof(State);
+  return Plan<HD, I8>::kState + sizeof(RingState<HD, I8>);
 }
 static_assert(smem_bytes<512, false>() <= 232448 && smem_bytes<512, true>() <= 232448 &&
                   smem_bytes<256, false>() <= 232448 && smem_bytes<256, true>() <= 232448,
@@ -273,67 +348,133 @@ Q4G_DEV float lane_sums(float (&v)[32], int lane) {
 }
 
 // -------------------------------------------------------------------- roles ----
-// Ring items in the order in which the products take them: per segment, in step i, the
-// K parts of tile i, then the V parts of tile i - 1. One thread.
-// (Asking L2 for the next tile as well, by prefetch copies, was slower at every length:
-// 16 sequences on a 128K prefix 178 us without, 200 us with.)
+// The scheduling warp works the segments out (their divisions and searches would cost each
+// role more than a microsecond a segment) and queues them; tiles = 0 ends the queue.
+struct Scheduler {
+  Work work;
+  Line line{};
+  Segment s{};
+  bool more;
+  int len;
+  uint32_t n = 0;
+  // before the CTA's first barrier: the first own lengths are asked for, and the first prefix
+  // segment comes from the arguments alone
+  Q4G_DEV Scheduler(const SharedParams& p, int lane) : work(p) {
+    len = lane < p.batch ? own_len_of(p, lane) : 0;
+    more = work.next(p, line, s);
+  }
+  Q4G_DEV bool push(const SharedParams& p, State& sh, int lane) {
+    if (n >= kQueue && !wait_warp(sh, p, &sh.seg_empty[n % kQueue], (n / kQueue - 1) & 1)) return false;
+    if (lane == 0) {
+      sh.seg[n % kQueue] = s;
+      mbar_arrive(&sh.seg_full[n % kQueue]);  // releases the write above
+    }
+    ++n;
+    return true;
+  }
+  Q4G_DEV void run(const SharedParams& p, State& sh, int lane) {
+    for (int kind = 0; kind < 2; ++kind) {
+      for (; more; more = work.next(p, line, s))
+        if (!push(p, sh, lane)) return;
+      if (kind == 0) {
+        sum_own_places(p, sh.own_places, lane, len);
+        __syncwarp();
+        line = make_line(p, sh.own_places);
+        work.start_own(p, line);
+        more = work.next(p, line, s);
+      }
+    }
+    s.tiles = 0;
+    push(p, sh, lane);
+  }
+};
+// A role's segment number i, false at the end (or when a wait has given up).
+Q4G_DEV bool take(State& sh, const SharedParams& p, uint32_t i, Segment& s) {
+  if (!wait(sh, p, &sh.seg_full[i % kQueue], (i / kQueue) & 1)) return false;
+  s = sh.seg[i % kQueue];
+  return s.tiles > 0;
+}
+Q4G_DEV void give_back(State& sh, uint32_t i) { mbar_arrive(&sh.seg_empty[i % kQueue]); }
+
+// A role's place in a ring of N stages and the phase that its next wait is for.
+template <int N>
+struct Ring {
+  int at = 0;
+  uint32_t phase;
+  Q4G_DEV explicit Ring(uint32_t first) : phase(first) {}
+  Q4G_DEV void step() {
+    if (++at == N) at = 0, phase ^= 1;
+  }
+};
+
+// All copies, by one thread: a segment's queries, then ring items in the order in which the
+// products take them: in step i the K parts of tile i, then the V parts of tile i - 1.
+// (Asking L2 for the next tile as well, by prefetch copies, was slower at every length.)
 template <int HD, bool I8>
-Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned char* smem, State& sh, const Line& w) {
+Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned char* smem, RingState<HD, I8>& sh) {
   using P = Plan<HD, I8>;
-  constexpr int NS = I8 ? P::kCodeStages : P::kStages;
+  constexpr int N = I8 ? P::kCodeStages : P::kStages;
+  Ring<N> r(1);  // the phase before a stage's first use: that wait is over at once
   uint64_t* const full = I8 ? sh.code_full : sh.full;
   uint64_t* const empty = I8 ? sh.code_empty : sh.empty;
-  const int64_t end = line_begin(w, blockIdx.x + 1);
-  uint32_t st = 0, phase = 1;  // the phase bit before a stage's first use: that wait is over at once
-  uint32_t it = 0;
+  uint32_t seg = 0, items = 0;
   bool ok = true;
-  for (int64_t t = line_begin(w, blockIdx.x); t < end && ok;) {
-    const Segment s = next_segment(p, w, t, end, blockIdx.x);
-    if (s.tiles == 0) continue;
+  Segment s{};
+  while (ok && take(sh, p, seg, s)) {
+    give_back(sh, seg);
+    if (seg > 0 && !(ok = wait(sh, p, &sh.q_free, (seg - 1) & 1))) break;
+    ++seg;
+    mbar_arrive_expect_tx(&sh.q_full, HD * 2 * p.heads * (s.own ? 1 : p.seqs));
+#pragma unroll 1
+    for (int c = 0; c < HD / 64; ++c)
+      tma_load_4d(smem + P::kQ + c * P::kQSlab, s.own ? &maps.own_q : &maps.q, c * 64, s.g0, s.h, s.b, &sh.q_full);
     for (int i = 0; i <= s.tiles && ok; ++i) {
       for (int part = 0; part < 2 && ok; ++part) {
         const int j = i - part;
         if (j < 0 || j >= s.tiles) continue;
         const void* const map = s.own ? (part ? &maps.own_v : &maps.own_k) : (part ? &maps.v : &maps.k);
-        const int key = (int)s.key0 + j * kTileKeys;
-        for (int c = 0; c < HD / 128; ++c, ++it) {
-          if (!(ok = wait(sh, p, &empty[st], phase))) break;
-          unsigned char* dst = smem + (I8 ? P::kCodes + st * P::kCodeStage : P::kRing + st * P::kStage);
-          mbar_arrive_expect_tx(&full[st], I8 ? P::kCodeStage : P::kStage);
+        const int key = s.key0 + j * kTileKeys;
+        for (int c = 0; c < HD / 128; ++c) {
+          if (!(ok = wait(sh, p, &empty[r.at], r.phase))) break;
+          unsigned char* dst = smem + (I8 ? P::kCodes + r.at * P::kCodeStage : P::kRing + r.at * P::kStage);
+          mbar_arrive_expect_tx(&full[r.at], I8 ? P::kCodeStage : P::kStage);
 #pragma unroll
           for (int half = 0; half < (I8 ? 1 : 2); ++half, dst += P::kSlab) {
             const int x = c * 128 + half * 64;
-            if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[st]);
-            else tma_load_3d(dst, map, x, s.h, key, &full[st]);
+            if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[r.at]);
+            else tma_load_3d(dst, map, x, s.h, key, &full[r.at]);
           }
-          if (++st == NS) st = 0, phase ^= 1;
+          r.step();
+          ++items;
         }
       }
     }
   }
   // Given up: the copies in flight still write this CTA's shared memory. Each is the last
   // of its stage, so its phase stays.
-  if (!ok)
-    for (uint32_t k = it > NS ? it - NS : 0; k < it; ++k) mbar_wait_bounded(&full[k % NS], (k / NS) & 1, p.wait_ns);
+  if (!ok || sh.abort) {
+    for (uint32_t k = items > N ? items - N : 0; k < items; ++k)
+      mbar_wait_bounded(&full[k % N], (k / N) & 1, 20000000ull);
+    if (seg > 0) mbar_wait_bounded(&sh.q_full, (seg - 1) & 1, 20000000ull);
+  }
 }
 
 // All products, by one thread.
 template <int HD, bool I8>
-Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, const Line& w) {
+Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, I8>& sh) {
   using P = Plan<HD, I8>;
-  constexpr int NS = P::kStages, C = HD / 128;
-  const uint32_t ring = smem_u32(smem) + P::kRing, q = smem_u32(smem) + P::kQ, pr = smem_u32(smem) + P::kP;
+  constexpr int C = HD / 128;
+  Ring<P::kStages> r(0);
+  const uint32_t ring = smem_u32(smem) + P::kRing, q = smem_u32(smem) + P::kQ, pt = smem_u32(smem) + P::kP;
   const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kGroupRows;
-  const int64_t end = line_begin(w, blockIdx.x + 1);
-  uint32_t st = 0, phase = 0, tile = 0, seg = 0;
+  uint32_t tile = 0, seg = 0;
   bool ok = true;
-  for (int64_t t = line_begin(w, blockIdx.x); t < end && ok;) {
-    const Segment s = next_segment(p, w, t, end, blockIdx.x);
-    if (s.tiles == 0) continue;
+  Segment s{};
+  while (ok && take(sh, p, seg, s)) {
+    give_back(sh, seg);
     const uint32_t n = (s.n_rows + 15) & ~15;
     const uint32_t id_s = tc_idesc_f16(n, false, false), id_o = tc_idesc_f16(n, true, true);
-    if (!(ok = wait(sh, p, &sh.q_ready, seg & 1))) break;
-    ++seg;
+    if (!(ok = wait(sh, p, &sh.q_full, seg & 1))) break;
     // Step i: S^T of tile i, then O^T += V^T P^T of tile i - 1, whose softmax ran while S^T
     // of tile i was made. (Part by part in turn, with a tile more between the two, was 7%
     // slower on 16 sequences and a 32K prefix: every part then pays the wait for its load.)
@@ -342,38 +483,40 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, con
         const uint32_t g = tile + i, s_at = s_col + (g & 1) * kGroupRows;
         if (g >= 2 && !(ok = wait(sh, p, &sh.s_free[g & 1], (g / 2 - 1) & 1))) break;
         for (int c = 0; c < C; ++c) {
-          if (!(ok = wait(sh, p, &sh.full[st], phase))) break;
+          if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
           tc_fence_after();
-          const uint32_t a = ring + st * P::kStage, b = q + 2 * c * P::kQSlab;
+          const uint32_t a = ring + r.at * P::kStage, b = q + 2 * c * P::kQSlab;
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             tc_mma_f16(s_at, tc_desc(a + (k >> 2) * P::kSlab + (k & 3) * 32, 0),
                        tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
-          tc_commit(&sh.empty[st]);
-          if (++st == NS) st = 0, phase ^= 1;
+          tc_commit(&sh.empty[r.at]);
+          r.step();
         }
         if (!ok) break;
         tc_commit(&sh.s_full[g & 1]);
+        if (i == s.tiles - 1) tc_commit(&sh.q_free);
       }
       if (i > 0) {
-        const uint32_t g = tile + i - 1, pt = pr + (g & 1) * P::kPBytes;
-        if (!(ok = wait(sh, p, &sh.p_full[g & 1], (g / 2) & 1))) break;
+        const uint32_t g = tile + i - 1;
+        if (i == 1 && seg > 0 && !(ok = wait(sh, p, &sh.o_free, (seg - 1) & 1))) break;
+        if (!(ok = wait(sh, p, &sh.p_full, g & 1))) break;
         // the live keys, rounded up to 16
-        const int live = min(kTileKeys, (int)(s.key_end - s.key0) - (i - 1) * kTileKeys);
+        const int live = min(kTileKeys, s.key_end - s.key0 - (i - 1) * kTileKeys);
         const int steps = (live + 15) >> 4;
         for (int c = 0; c < C; ++c) {
-          if (!(ok = wait(sh, p, &sh.full[st], phase))) break;
+          if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
+          const int at = P::kRing + r.at * P::kStage;
           if (!I8 && s.own && live < steps * 16) {
             // what lies behind a sequence's own rows may be anything, and zero times a NaN
             // is not zero
             for (int x = live * 8; x < steps * 128; ++x)
               for (int half = 0; half < 2; ++half)
-                *reinterpret_cast<uint4*>(smem + P::kRing + st * P::kStage + half * P::kSlab + x * 16) =
-                    make_uint4(0, 0, 0, 0);
+                *reinterpret_cast<uint4*>(smem + at + half * P::kSlab + x * 16) = make_uint4(0, 0, 0, 0);
             fence_async_smem();
           }
           tc_fence_after();
-          const uint32_t a = ring + st * P::kStage, o_at = o_col + c * kGroupRows;
+          const uint32_t a = smem_u32(smem) + at, o_at = o_col + c * kGroupRows;
           if (steps == kTileKeys / 16) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -382,16 +525,17 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, State& sh, con
             for (int k = 0; k < steps; ++k)
               tc_mma_f16(o_at, tc_desc(a + k * 2048, P::kSlab), tc_desc(pt + k * 2048, 0), id_o, i > 1 || k > 0);
           }
-          tc_commit(&sh.empty[st]);
-          if (++st == NS) st = 0, phase ^= 1;
+          tc_commit(&sh.empty[r.at]);
+          r.step();
         }
         if (!ok) break;
-        tc_commit(&sh.pv_done[g & 1]);
+        tc_commit(&sh.pv_done);
       }
     }
     tile += s.tiles;
+    ++seg;
   }
-  if (!ok) {  // given up: products in flight still use shared and tensor memory
+  if (!ok || sh.abort) {  // given up: products in flight still use shared and tensor memory
     tc_commit(&sh.drain);
     mbar_wait_bounded(&sh.drain, 0, p.wait_ns);
   }
@@ -408,14 +552,19 @@ Q4G_DEV uint32_t widen2(uint32_t u, uint32_t sel) {
 constexpr int kGroup = kConvertWarps / 2 * 32;
 
 template <int HD>
-Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, State& sh, const Line& w) {
+Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh) {
   using P = Plan<HD, true>;
   constexpr int NS = P::kStages, NC = P::kCodeStages, C = HD / 128;
   const int tid = threadIdx.x - 32 * (4 + kSoftmaxWarps), lane = tid & 31, group = tid / kGroup;
-  const int64_t end = line_begin(w, blockIdx.x + 1);
-  uint32_t items = 0;
-  for (int64_t t = line_begin(w, blockIdx.x); t < end;) items += 2 * C * next_segment(p, w, t, end, blockIdx.x).tiles;
-  for (uint32_t it = group; it < items; it += 2) {
+  uint32_t items = 0, seg = 0;
+  for (uint32_t it = group;; it += 2) {
+    while (it >= items) {
+      Segment s;
+      if (!__all_sync(0xffffffffu, take(sh, p, seg, s))) return;
+      if (lane == 0) give_back(sh, seg);
+      ++seg;
+      items += 2 * C * s.tiles;
+    }
     const uint32_t cs = it % NC, st = it % NS;
     if (!wait_warp(sh, p, &sh.code_full[cs], (it / NC) & 1)) return;
     if (it >= NS && !wait_warp(sh, p, &sh.empty[st], (it / NS - 1) & 1)) return;
@@ -444,58 +593,27 @@ Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, State& sh, cons
 
 // One thread: a key of the tile (tensor-memory lane) and 32 of the 64 query rows.
 template <int HD, bool I8>
-Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, const Line& w) {
+Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh) {
   using P = Plan<HD, I8>;
   constexpr int C = HD / 128;
   const int tid = threadIdx.x - 128, lane = tid & 31, quarter = (tid >> 5) & 3, c0 = (tid >> 7) * 32;
   const int key = quarter * 32 + lane;
   const uint32_t lanes = sh.tmem + ((uint32_t)(quarter * 32) << 16);
   const uint32_t s_col = lanes + c0, o_col = lanes + 2 * kGroupRows + c0;
-  const int64_t end = line_begin(w, blockIdx.x + 1);
   uint32_t tile = 0;
   // once a wait has given up nothing waits any more, but every thread goes on to the end:
   // the barriers among these warps have no limit of their own
   bool ok = true;
-  for (int64_t t = line_begin(w, blockIdx.x); t < end;) {
-    const Segment s = next_segment(p, w, t, end, blockIdx.x);
-    if (s.tiles == 0) continue;
+  for (uint32_t seg = 0;; ++seg) {
+    Segment s;
+    if (softmax_any(!__all_sync(0xffffffffu, take(sh, p, seg, s)))) break;  // all warps or none
+    if (lane == 0) give_back(sh, seg);
     const int n = (s.n_rows + 15) & ~15;
-    // the unit's query rows, zeros behind them; eight loads of a thread in flight. CTAs
-    // start at different rows: most of them read the same ones at the same time
-    constexpr int kRowsAtOnce = kSoftmaxThreads / (HD / 8);
-    const int ch = tid % (HD / 8);
-    const __half* const q_head = p.q + (int64_t)s.h * p.G * HD + ch * 8;
-    unsigned char* const q_dst = smem + P::kQ + (ch >> 3) * P::kQSlab;
-    const int turn = (blockIdx.x * 4) % n;
-    const float inv_G = 1.0f / p.G;
-    for (int r0 = tid / (HD / 8); r0 < n; r0 += 8 * kRowsAtOnce) {
-      uint4 v[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = r0 + i * kRowsAtOnce + turn;
-        const int r = at < n ? at : at - n, rr = s.row0 + r;
-        // rr / G: the quotient is off by less than 2^-23 of itself, rr < 2^18 and G <= 1024 put
-        // (rr + 1/2) / G at least 2^-11 from a whole number while it is below 2^18 / G
-        const int b = s.own ? s.b : (int)((rr + 0.5f) * inv_G), g = s.own ? rr : rr - b * p.G;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (r < s.n_rows && at - turn < n) v[i] = __ldg(reinterpret_cast<const uint4*>(q_head + ((int64_t)b * p.n_q + g) * HD));
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int at = r0 + i * kRowsAtOnce + turn;
-        const int r = at < n ? at : at - n;
-        if (at - turn < n) *reinterpret_cast<uint4*>(q_dst + r * 128 + (((ch & 7) ^ (r & 7)) * 16)) = v[i];
-      }
-    }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.q_ready);
-
     float l[32];
 #pragma unroll
     for (int i = 0; i < 32; ++i) l[i] = 0.f;
-    int left = (int)(s.key_end - s.key0) - key;  // this thread's key of the tile is live while left > 0
-    const int64_t row0 = ((int64_t)s.b * p.own_cap + s.key0 + key) * p.n_kv + s.h;  // s.b = 0 over the prefix
+    int left = s.key_end - s.key0 - key;  // this thread's key of the tile is live while left > 0
+    const int64_t row0 = ((s.own ? (int64_t)s.b * p.own_cap : 0) + s.key0 + key) * p.n_kv + s.h;
     const float* ks_at = (s.own ? p.ks[1] : p.ks[0]) + row0;
     const float* vs_at = (s.own ? p.vs[1] : p.vs[0]) + row0;
     for (int j = 0; j < s.tiles; ++j, ++tile, left -= kTileKeys) {
@@ -539,13 +657,12 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
         const float m = fmaxf(fmaxf(fmaxf(sh.wmax[0][tid], sh.wmax[1][tid]), fmaxf(sh.wmax[2][tid], sh.wmax[3][tid])),
                               -1e30f);
         const float old = sh.ref[tid];
-        raise = j > 0 && m > old + kHeadroom;
+        raise = j > 0 && tid < s.n_rows && m > old + kHeadroom;  // rows of padding hold anything
         sh.factor[tid] = raise ? ex2(old - m) : 1.f;
         if (j == 0 || raise) sh.ref[tid] = m;
       }
       raise = softmax_any(raise);
-      if (raise) ok = ok && wait_warp(sh, p, &sh.pv_done[buf ^ 1], ((tile - 1) / 2) & 1);  // O^T is free
-      else if (j >= 2) ok = ok && wait_warp(sh, p, &sh.pv_done[buf], (tile / 2 - 1) & 1);  // this P^T is free
+      if (j > 0) ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);  // P^T and O^T are free
       if (active) {
         if (raise) {
           tc_fence_after();
@@ -565,7 +682,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
 #pragma unroll
           for (int i = 0; i < 32; ++i) l[i] *= sh.factor[c0 + i];
         }
-        unsigned char* const row = smem + P::kP + buf * P::kPBytes + key * 128;
+        unsigned char* const row = smem + P::kP + key * 128;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           uint32_t h[4];
@@ -583,28 +700,33 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh, cons
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[buf]);
+      if (lane == 0) mbar_arrive(&sh.p_full);
     }
 
-    // the segment's partial
-    ok = ok && wait_warp(sh, p, &sh.pv_done[(tile - 1) & 1], ((tile - 1) / 2) & 1);
+    // the segment's partial: thread = value dimension and, of up to 32 rows, half of the
+    // dimension blocks each; of more, half of the rows
+    ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);
     tc_fence_after();
-    softmax_sync();  // wmax is free
     float* const ml = (s.own ? p.own_ml : p.ml) + s.slot * (s.own ? p.own_rows : p.rows) * 2;
-    float* const acc = (s.own ? p.own_acc : p.acc) + s.slot * (s.own ? p.own_rows : p.rows) * HD;
-    if (c0 < n) {
-      sh.wmax[quarter][c0 + lane] = lane_sums(l, lane);
+    float* const acc = (s.own ? p.own_acc : p.acc) + s.slot * (s.own ? p.own_rows : p.rows) * HD + key;
+    if (c0 < n) sh.wmax[quarter][c0 + lane] = lane_sums(l, lane);
+    const bool few = n <= 32;
+    const int r0 = few ? 0 : c0, first = few && c0 > 0 ? C / 2 : 0, last = few && c0 == 0 ? C / 2 : C;
 #pragma unroll 1
-      for (int c = 0; c < C; ++c) {
-        float o[32];
-        tmem_ld32(o_col + c * kGroupRows, o);
-        tmem_wait_ld(o);
-#pragma unroll
-        for (int i = 0; i < 32; ++i)
-          if (c0 + i < s.n_rows) acc[(int64_t)(c0 + i) * HD + c * 128 + key] = o[i];
+    for (int c = first; c < last; ++c) {
+      float o[32];
+      tmem_ld32(lanes + 2 * kGroupRows + c * kGroupRows + r0, o);
+      tmem_wait_ld(o);
+      if (c == last - 1) {  // O^T may be written again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_free);
       }
+      float* const at = acc + r0 * HD + c * 128;
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (r0 + i < s.n_rows) at[i * HD] = o[i];
     }
-    tc_fence_before();
     softmax_sync();
     if (tid < s.n_rows) {
       ml[2 * tid] = sh.ref[tid];
@@ -618,26 +740,33 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     shared_kernel(const __grid_constant__ SharedMaps maps, const SharedParams p) {
   using P = Plan<HD, I8>;
   extern __shared__ __align__(1024) unsigned char smem[];
-  State& sh = *reinterpret_cast<State*>(smem + P::kState);
+  RingState<HD, I8>& sh = *reinterpret_cast<RingState<HD, I8>*>(smem + P::kState);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 0) {
-    sum_own_places(p, sh.own_places, lane);
-  } else if (warp == 1) {
+  Scheduler scheduler(p, lane);  // (warp 3's)
+  if (warp == 1) {
     tmem_alloc(&sh.tmem, 512);
   } else if (warp == 2 && lane == 0) {
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < P::kStages; ++i) {
       mbar_init(&sh.full[i], I8 ? kConvertWarps / 2 : 1);
       mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < P::kCodeStages; ++i) {
       mbar_init(&sh.code_full[i], 1);
       mbar_init(&sh.code_empty[i], kConvertWarps / 2);
+    }
+    for (int i = 0; i < kQueue; ++i) {
+      mbar_init(&sh.seg_full[i], 1);
+      mbar_init(&sh.seg_empty[i], 2 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kSoftmaxWarps);
-      mbar_init(&sh.p_full[i], kSoftmaxWarps);
-      mbar_init(&sh.pv_done[i], 1);
     }
-    mbar_init(&sh.q_ready, kSoftmaxWarps);
+    mbar_init(&sh.p_full, kSoftmaxWarps);
+    mbar_init(&sh.pv_done, 1);
+    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_free, 1);
+    mbar_init(&sh.o_free, kSoftmaxWarps);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     fence_mbar_init();
@@ -646,26 +775,27 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const Line w = make_line(p, sh.own_places);
   pdl_launch_dependents();  // the join's CTAs take the places that CTAs of this grid leave
-  // With int8 rows 640 threads start with 96 registers each: the softmax warps take 136,
-  // 4 x 32 x (56 + 2 x 136 + 2 x 72) = 472 x 128 of 480 x 128.
+  // With int8 rows 640 threads start with 96 registers each: the softmax warps take 128,
+  // (72 + 2 x 128 + 2 x 72) x 128 = 472 x 128 of 480 x 128.
   if (warp < 4) {
-    if constexpr (I8) regs_dec<56>();
+    if constexpr (I8) regs_dec<72>();
     if (warp == 0) {
-      if (elect_one()) produce<HD, I8>(p, maps, smem, sh, w);
+      if (elect_one()) produce<HD, I8>(p, maps, smem, sh);
       __syncwarp();
     } else if (warp == 1) {
-      if (elect_one()) multiply<HD, I8>(p, smem, sh, w);
+      if (elect_one()) multiply<HD, I8>(p, smem, sh);
       __syncwarp();
+    } else if (warp == 3) {
+      scheduler.run(p, sh, lane);
     }
   } else if (warp < 4 + kSoftmaxWarps) {
-    if constexpr (I8) regs_inc<136>();
-    softmax<HD, I8>(p, smem, sh, w);
+    if constexpr (I8) regs_inc<128>();
+    softmax<HD, I8>(p, smem, sh);
   } else {
     if constexpr (I8) {
       regs_dec<72>();
-      convert<HD>(p, smem, sh, w);
+      convert<HD>(p, smem, sh);
     }
   }
   tc_fence_before();
@@ -677,23 +807,22 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
 }
 
 // ------------------------------------------------------------------ the join ----
-constexpr int kJoinThreads = 512;
-constexpr int kJoinCols = 128;                          // output columns per CTA
-constexpr int kJoinLanes = kJoinCols / 4;               // threads across them: a warp
-constexpr int kJoinParts = kJoinThreads / kJoinLanes;   // threads down the partials: the warps
+constexpr int kJoinCols = 128;                          // output columns per CTA: four a lane
 constexpr int kJoinMax = 2 * 256;                       // partials of a row: CTAs of its two units
 
 // out[row] = sum_i 2^(ref_i - R) O_i / sum_i 2^(ref_i - R) l_i over the row's partials,
 // R the largest reference; in a fixed order. Grid: query rows, columns / 128. The weights
 // are made once, one thread a partial, so that the loads of O depend on nothing.
-template <int HD>
-__global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedParams p) {
+// kJoinParts warps, each with every kJoinParts-th partial.
+template <int HD, int kJoinParts>
+__global__ void __launch_bounds__(32 * kJoinParts) shared_join_kernel(const SharedParams p) {
+  constexpr int kJoinThreads = 32 * kJoinParts, kJoinLanes = 32;
   __shared__ int32_t own_places[kMaxBatch + 1];
   __shared__ float red[2][kJoinThreads / 32];
   __shared__ float weight[kJoinMax];
   __shared__ float4 part[kJoinParts][kJoinLanes];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  if (warp == 0) sum_own_places(p, own_places, lane);
+  if (warp == 0) sum_own_places(p, own_places, lane, lane < p.batch ? own_len_of(p, lane) : 0);
   __syncthreads();
   const Line w = make_line(p, own_places);
   const int b = blockIdx.x / p.n_q, hq = blockIdx.x % p.n_q, h = hq / p.G, g = hq % p.G;
@@ -701,29 +830,46 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
   // the partials of the row: slots [s0, s0 + n0) of the prefix, [s1, s1 + n1) of its own rows
   int64_t s0 = 0, s1 = 0;
   int n0 = 0, n1 = 0, r0 = 0, r1 = g % kGroupRows;
-  if (w.prefix > 0) {
-    const int rr = b * p.G + g;
-    const int64_t u = (int64_t)h * p.groups + rr / kGroupRows, t = u * w.prefix;
-    const int c = line_cta(w, t + kUnitCost);
-    r0 = rr % kGroupRows;
-    s0 = u + c;
-    n0 = line_cta(w, t + w.prefix - 1) - c + 1;
+  if (p.prefix_tiles > 0) {
+    const int u = h * p.groups + (p.parts == 1 ? b / p.seqs : b * p.parts + g / kGroupRows);
+    r0 = p.parts == 1 ? b % p.seqs * p.G + g : g % kGroupRows;
+    if (p.pieces > 0) {
+      s0 = (int64_t)u * p.pieces;
+      n0 = p.pieces;
+    } else {
+      const int64_t len = places(p.prefix_tiles), total = len * p.n_kv * p.groups;
+      const int c = cut_of(total, p.prefix_ctas, u * len + kUnitCost);
+      s0 = (int64_t)u + c;
+      n0 = cut_of(total, p.prefix_ctas, u * len + len - 1) - c + 1;
+    }
   }
   const int own = own_places[b + 1] - own_places[b];
   if (own > 0) {
-    const int per = p.n_kv * p.own_groups, u = h * p.own_groups + g / kGroupRows;
-    const int64_t t = (int64_t)p.n_kv * p.groups * w.prefix + (int64_t)own_places[b] * per + (int64_t)u * own;
-    const int c = line_cta(w, t + kUnitCost);
+    const int per = p.n_kv * p.parts, u = h * p.parts + g / kGroupRows;
+    const int64_t t = (int64_t)own_places[b] * per + (int64_t)u * own;
+    const int c = line_piece(w, t + kUnitCost);
     s1 = (int64_t)b * per + u + c;
-    n1 = line_cta(w, t + own - 1) - c + 1;
+    n1 = line_piece(w, t + own - 1) - c + 1;
   }
   const int n = n0 + n1;
-  // references, sums and weights, one partial a thread (n <= 2 * CTAs <= kJoinMax)
+  const float* const acc0 = p.acc + (s0 * p.rows + r0) * HD + blockIdx.y * kJoinCols + lane * 4;
+  const float* const acc1 = p.own_acc + (s1 * p.own_rows + r1) * HD + blockIdx.y * kJoinCols + lane * 4;
+  const int64_t step0 = (int64_t)p.rows * HD, step1 = (int64_t)p.own_rows * HD;
+  auto o_at = [&](int i) {
+    return *reinterpret_cast<const float4*>(i < n0 ? acc0 + i * step0 : acc1 + (i - n0) * step1);
+  };
+  // references, sums and weights, a partial a thread and turn (n <= 2 * CTAs <= kJoinMax); a
+  // warp's first rows of O are loaded beside them
+  constexpr int kEarly = 5;
+  float4 early[kEarly];
   const float* const ml0 = p.ml + (s0 * p.rows + r0) * 2;
   const float* const ml1 = p.own_ml + (s1 * p.own_rows + r1) * 2;
   float2 ml[kJoinMax / kJoinThreads];
   float R = -INFINITY;
   pdl_wait();  // all above comes from the call's own arguments
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (warp + k * kJoinParts < n) early[k] = o_at(warp + k * kJoinParts);
 #pragma unroll
   for (int k = 0; k < kJoinMax / kJoinThreads; ++k) {
     const int i = tid + k * kJoinThreads;
@@ -751,16 +897,13 @@ __global__ void __launch_bounds__(kJoinThreads) shared_join_kernel(const SharedP
   l = warp_sum(l);
   if (lane == 0) red[1][warp] = l;
   __syncthreads();
-  const float* const acc0 = p.acc + (s0 * p.rows + r0) * HD + blockIdx.y * kJoinCols + lane * 4;
-  const float* const acc1 = p.own_acc + (s1 * p.own_rows + r1) * HD + blockIdx.y * kJoinCols + lane * 4;
-  const int64_t step0 = (int64_t)p.rows * HD, step1 = (int64_t)p.own_rows * HD;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 10
-  for (int i = warp; i < n; i += kJoinParts) {
-    const float4 a = *reinterpret_cast<const float4*>(i < n0 ? acc0 + i * step0 : acc1 + (i - n0) * step1);
-    const float f = weight[i];
-    o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w;
-  }
+  auto add = [&](float4 a, float f) { o.x += f * a.x, o.y += f * a.y, o.z += f * a.z, o.w += f * a.w; };
+#pragma unroll
+  for (int k = 0; k < kEarly; ++k)
+    if (warp + k * kJoinParts < n) add(early[k], weight[warp + k * kJoinParts]);
+#pragma unroll 5
+  for (int i = warp + kEarly * kJoinParts; i < n; i += kJoinParts) add(o_at(i), weight[i]);
   part[warp][lane] = o;
   __syncthreads();
   if (warp == 0) {
@@ -803,20 +946,43 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// Rows [batch][rows][n_kv][hd] of fp16 or codes; a box is 128 keys of one KV head and 64
-// fp16 columns (swizzled) or 128 codes. Keys past `rows` read as zeros. batch 0: [rows][n_kv][hd].
-bool encode(CUtensorMap* m, const void* base, int hd, int n_kv, int64_t rows, int batch, bool i8) {
-  const cuuint64_t e = i8 ? 1 : 2;
-  const cuuint64_t dims[4] = {(cuuint64_t)hd, (cuuint64_t)n_kv, (cuuint64_t)rows, (cuuint64_t)batch};
-  const cuuint64_t strides[3] = {hd * e, (cuuint64_t)n_kv * hd * e, (cuuint64_t)rows * n_kv * hd * e};
-  const cuuint32_t box[4] = {i8 ? 128u : 64u, 1, kTileKeys, 1}, one[4] = {1, 1, 1, 1};
-  return encode_tiled()(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, batch ? 4 : 3,
-                        const_cast<void*>(base), dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+// A tensor map over fp16 values (boxes of 64 columns, swizzled) or codes (128 columns).
+// dims and box from the columns outwards, `rank` of them; stride[i]: elements between
+// neighbours of dimension i + 1. What a box has outside the tensor reads as zeros.
+bool encode(CUtensorMap* m, const void* base, bool i8, int rank, const int64_t* dims, const int64_t* stride,
+            const int32_t* box) {
+  cuuint64_t d[4], s[3];
+  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) d[i] = (cuuint64_t)dims[i], b[i] = (cuuint32_t)box[i];
+  for (int i = 0; i + 1 < rank; ++i) s[i] = (cuuint64_t)stride[i] * (i8 ? 1 : 2);
+  return encode_tiled()(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                        const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
                         i8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Rows [batch][rows][n_kv][hd]; a box is 128 keys of one KV head.
+bool encode_rows(CUtensorMap* m, const void* base, bool i8, int rank, int hd, int n_kv, int64_t rows, int batch) {
+  const int64_t dims[] = {hd, n_kv, rows, batch}, stride[] = {hd, (int64_t)n_kv * hd, rows * n_kv * hd};
+  const int32_t box[] = {i8 ? 128 : 64, 1, kTileKeys, 1};
+  return encode(m, base, i8, rank, dims, stride, box);
+}
+
 constexpr int kMaxDevices = 64;
+
+template <int HD, int kJoinParts>
+cudaError_t launch_join(const SharedParams& p, cudaStream_t st) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(p.batch * p.n_q, HD / kJoinCols);
+  cfg.blockDim = dim3(32 * kJoinParts);
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, shared_join_kernel<HD, kJoinParts>, p);
+}
 
 template <int HD, bool I8>
 cudaError_t launch(const SharedMaps& maps, const SharedParams& p, cudaStream_t st) {
@@ -837,29 +1003,53 @@ cudaError_t launch(const SharedMaps& maps, const SharedParams& p, cudaStream_t s
   }
   shared_kernel<HD, I8><<<p.ctas, Plan<HD, I8>::kThreads, smem_bytes<HD, I8>(), st>>>(maps, p);
   if ((e = cudaGetLastError()) != cudaSuccess) return e;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.batch * p.n_q, HD / kJoinCols);
-  cfg.blockDim = dim3(kJoinThreads);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_join_kernel<HD>, p);
+  // warps for about five partials each
+  const int n = (p.pieces > 0 ? p.pieces : p.prefix_tiles > 0 ? 2 : 0) + (p.own_cap + kTileKeys - 1) / kTileKeys;
+  if (n <= 20) return launch_join<HD, 4>(p, st);
+  return n <= 40 ? launch_join<HD, 8>(p, st) : launch_join<HD, 16>(p, st);
+}
+
+// How the prefix units are cut: into equal pieces of `len` tiles, or, where whole pieces
+// would leave more than a tenth of the CTAs without work, as one line. A longer piece
+// leaves CTAs for the own rows, which otherwise come on top of somebody's piece: the
+// length with the smallest estimate of the longest CTA's tiles is taken, own rows at
+// half of their capacity (their lengths are on the device).
+void plan_prefix(SharedParams& p, int64_t prefix, int64_t own_cap) {
+  p.prefix = (int32_t)prefix;
+  p.prefix_tiles = (int32_t)((prefix + kTileKeys - 1) / kTileKeys);
+  p.pieces = p.prefix_ctas = 0;
+  if (prefix == 0) return;
+  const int64_t units = (int64_t)p.n_kv * p.groups, tiles = p.prefix_tiles, most = p.ctas / units;
+  if (most < tiles && most * units * 10 < 9 * (int64_t)p.ctas) {
+    p.prefix_ctas = p.ctas;  // units * (tiles + 1) > ctas places: no piece of the line is empty
+    return;
+  }
+  const int64_t own = own_cap == 0 ? 0 : (int64_t)p.batch * p.n_kv * p.parts * ((own_cap / 2) / kTileKeys + 1 + kUnitCost);
+  int64_t best = 0;
+  const int64_t least = (tiles + most - 1) / most;
+  for (int64_t len = least; len <= least + 4 && len <= tiles; ++len) {
+    const int64_t pieces = (tiles + len - 1) / len, load = (tiles + pieces - 1) / pieces + kUnitCost;
+    const int64_t idle = p.ctas - pieces * units, over = own - idle * load;
+    // what the idle CTAs cannot take is shared by all, whole units at a time
+    const int64_t cost = over <= 0 ? load : load + 1 + (over + p.ctas - 1) / p.ctas;
+    if (best == 0 || cost < best) best = cost, p.pieces = (int32_t)pieces;
+  }
+  p.prefix_ctas = (int32_t)(p.pieces * units);
 }
 
 // Units, partial slots and the scratch layout; returns its bytes.
 size_t plan_scratch(SharedParams& p, int hd, void* ws) {
   p.G = p.n_q / p.n_kv;
-  const int rows = p.batch * p.G;
-  p.groups = (rows + kGroupRows - 1) / kGroupRows;
-  p.own_groups = (p.G + kGroupRows - 1) / kGroupRows;
-  p.rows = rows < kGroupRows ? rows : kGroupRows;
-  p.own_rows = p.G < kGroupRows ? p.G : kGroupRows;
+  p.parts = (p.G + kGroupRows - 1) / kGroupRows;
+  p.seqs = p.parts == 1 ? kGroupRows / p.G : 1;
+  if (p.seqs > p.batch) p.seqs = p.batch;
+  p.heads = p.parts == 1 ? p.G : kGroupRows;
+  p.groups = p.parts == 1 ? (p.batch + p.seqs - 1) / p.seqs : p.batch * p.parts;
+  p.rows = p.seqs * p.heads;
+  p.own_rows = p.heads;
   p.ctas = device_sm_count() < kJoinMax / 2 ? device_sm_count() : kJoinMax / 2;
   const size_t n = ((size_t)p.n_kv * p.groups + p.ctas) * p.rows;
-  const size_t n_own = ((size_t)p.batch * p.n_kv * p.own_groups + p.ctas) * p.own_rows;
+  const size_t n_own = ((size_t)p.batch * p.n_kv * p.parts + p.ctas) * p.own_rows;
   size_t off = 0;
   auto take = [&](size_t floats) {
     float* at = reinterpret_cast<float*>(reinterpret_cast<char*>(ws) + off);
@@ -907,20 +1097,24 @@ q4g_status run_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_k
   for (const void* x : ptrs)
     if (x && !on_current_device(x)) return bad(Q4G_EINVAL, "a pointer is not memory of the current device");
   if (!encode_tiled()) return bad(Q4G_ECUDA, "the driver has no tensor maps");
-  p.q = reinterpret_cast<const __half*>(q);
   p.ks[0] = kps, p.ks[1] = kos, p.vs[0] = vps, p.vs[1] = vos;
-  p.prefix = prefix;
+  plan_prefix(p, prefix, own_cap);
   p.own_cap = (int32_t)own_cap;
   p.own_len = own_len;
   p.out = reinterpret_cast<__half*>(out);
   p.wait_ns = 2000000000ull;
   if (!(p.err = device_error_word())) return bad(Q4G_ECUDA, "error word unavailable");
   SharedMaps maps{};
-  bool ok = true;
-  if (prefix > 0) ok = encode(&maps.k, kp, hd, n_kv, prefix, 0, i8) && encode(&maps.v, vp, hd, n_kv, prefix, 0, i8);
+  // queries as [batch][n_kv][G][hd]: a box is the rows of a unit
+  const int64_t q_dims[] = {hd, p.G, n_kv, batch}, q_stride[] = {hd, (int64_t)p.G * hd, (int64_t)n_q * hd};
+  const int32_t q_box[] = {64, p.heads, 1, p.seqs}, own_q_box[] = {64, p.heads, 1, 1};
+  bool ok = encode(&maps.q, q, false, 4, q_dims, q_stride, q_box) &&
+            encode(&maps.own_q, q, false, 4, q_dims, q_stride, own_q_box);
+  if (prefix > 0)
+    ok = ok && encode_rows(&maps.k, kp, i8, 3, hd, n_kv, prefix, 1) && encode_rows(&maps.v, vp, i8, 3, hd, n_kv, prefix, 1);
   if (own_cap > 0)
-    ok = ok && encode(&maps.own_k, ko, hd, n_kv, own_cap, batch, i8) &&
-         encode(&maps.own_v, vo, hd, n_kv, own_cap, batch, i8);
+    ok = ok && encode_rows(&maps.own_k, ko, i8, 4, hd, n_kv, own_cap, batch) &&
+         encode_rows(&maps.own_v, vo, i8, 4, hd, n_kv, own_cap, batch);
   if (!ok) return bad(Q4G_ECUDA, "tensor map refused by the driver");
   cudaError_t e;
   if (hd == 512) e = i8 ? launch<512, true>(maps, p, st) : launch<512, false>(maps, p, st);
