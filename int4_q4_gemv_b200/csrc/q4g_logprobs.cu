@@ -6,10 +6,12 @@
 // Bound by HBM: 4 bytes per logit, read once. Every thread keeps its own running
 // (m, S, E = sum exp(d) d) and rescales them when its maximum moves; E counts from
 // the maximum, so the entropy is a sum of terms of one sign and cancels nothing.
-// The alternatives come out of the same pass: logits at or above a threshold enter
-// a candidate buffer in shared memory, and the threshold is always a value that at
-// least n_top logits of the row reach (first from the lane maxima of a warp, then
-// the n_top-th best candidate), so nothing that belongs to the answer is left out.
+// The alternatives cost the pass nothing: it leaves every thread's largest logit, and the
+// n_top best logits of a CTA's part lie with the threads whose largest is at least the
+// n_top-th largest of those (n_top logits reach it). Only these threads' logits, n_top of
+// 256 or 1024 shares, are read again, from L2. (Lists kept up to date while reading, per
+// CTA or per warp, took 98 and 106 us on 256 rows of 262,144 logits with 20 alternatives,
+// 52 and 60 more than without alternatives.)
 // A row is split over the CTAs of one thread-block cluster when there are few rows;
 // they join through distributed shared memory, in rank order, without scratch memory
 // or atomics between CTAs: the sums do not depend on timing, nor does the answer on
@@ -24,14 +26,10 @@ using namespace q4g;
 
 namespace {
 
-constexpr int kLpThreads = 256;
-constexpr int kLpWarps = kLpThreads / 32;
-constexpr int kVecs = 4;                            // 16-byte loads per thread and tile
-constexpr int kTile = kLpThreads * kVecs * 4;       // logits per tile
-constexpr int kKeep = 128;                          // candidates that may wait for the next tile
-constexpr int kBuf = kTile + kKeep;
-constexpr int kMaxCluster = 8;
-static_assert(kMaxCluster <= kLpWarps, "one warp merges one CTA's list");
+constexpr int kVecs = 4;           // 16-byte loads per thread and tile
+constexpr int kMaxCluster = 8;     // no more than a CTA's warps: one merges one CTA's list
+constexpr int kSmall = 256, kLarge = 1024;  // threads per CTA
+constexpr int tile_of(int threads) { return threads * kVecs * 4; }  // logits per tile
 
 typedef unsigned long long u64;
 
@@ -77,12 +75,14 @@ Q4G_DEV K sort_desc(K v, int lane) {
     for (int o = k >> 1; o > 0; o >>= 1) v = cmp_swap(v, o, ((lane & o) != 0) == ((lane & k) == 0));
   return bitonic_merge_desc(v, lane);
 }
+Q4G_DEV uint32_t shfl_key(uint32_t v, int src) { return __shfl_sync(0xffffffffu, v, src); }
+Q4G_DEV u64 shfl_key(u64 v, int src) {
+  return ((u64)shfl_key((uint32_t)(v >> 32), src) << 32) | shfl_key((uint32_t)v, src);
+}
 // The 32 best of two lists in falling order, in falling order.
-Q4G_DEV u64 merge_lists(u64 a, u64 b, int lane) {
-  const int src = 31 - lane;
-  const uint32_t lo = __shfl_sync(0xffffffffu, (uint32_t)b, src);
-  const uint32_t hi = __shfl_sync(0xffffffffu, (uint32_t)(b >> 32), src);
-  const u64 r = ((u64)hi << 32) | lo;
+template <typename K>
+Q4G_DEV K merge_lists(K a, K b, int lane) {
+  const K r = shfl_key(b, 31 - lane);
   return bitonic_merge_desc(a > r ? a : r, lane);
 }
 
@@ -107,13 +107,15 @@ Q4G_DEV Stat stat_join(Stat a, Stat b, float c) {
   return {m, a.l * wa + b.l * wb, (a.e + da * a.l) * wa + (b.e + db * b.l) * wb};
 }
 
+template <int THREADS>
 struct LpShared {
-  u64 lists[kLpWarps][32];  // per-warp lists while merging; [0] is the CTA's list
-  u64 best;                 // the n_top-th best key so far (0: none)
-  Stat warp_stat[kLpWarps];
+  u64 lists[THREADS / 32][32];  // the warps' lists while merging; [0] is then the CTA's
+  u64 wait[THREADS / 32][64];   // a warp's candidates until they are 32
+  Stat warp_stat[THREADS / 32];
   Stat stat;
-  uint32_t warp_thr[kLpWarps];
-  int count;                // candidates in the buffer
+  uint32_t maxima[THREADS / 32][32];  // as lists, of the threads' largest logits (keys' high words)
+  uint16_t hits[THREADS];       // threads to read again
+  int n_hits;
 };
 
 Q4G_DEV u64 ld_peer_u64(uint32_t addr) {
@@ -122,38 +124,114 @@ Q4G_DEV u64 ld_peer_u64(uint32_t addr) {
   return v;
 }
 
-// The 32 best of the candidate buffer and of the list already held (lists[0], as
-// candidates of their own when `held`), into lists[0]. All threads call it.
-Q4G_DEV void compact(LpShared& sh, const u64* buf, int count, bool held, int n_top) {
+// The warps' lists, each in falling order, into one: the 32 best, in lists[0]. All threads
+// call it; it ends with a barrier.
+template <int WARPS, typename K>
+Q4G_DEV void merge_warps(K (&lists)[WARPS][32], K best) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  u64 best = warp == 0 && held ? sh.lists[0][lane] : 0ull;
-  for (int b = warp * 32; b < count; b += kLpThreads) {
-    const u64 k = b + lane < count ? buf[b + lane] : 0ull;
-    best = merge_lists(best, sort_desc(k, lane), lane);
-  }
-  sh.lists[warp][lane] = best;
+  lists[warp][lane] = best;
   __syncthreads();
 #pragma unroll
-  for (int s = 1; s < kLpWarps; s <<= 1) {
+  for (int s = 1; s < WARPS; s <<= 1) {
     if (warp % (2 * s) == 0) {
-      best = merge_lists(best, sh.lists[warp + s][lane], lane);
-      sh.lists[warp][lane] = best;
+      best = merge_lists(best, lists[warp + s][lane], lane);
+      lists[warp][lane] = best;
     }
     __syncthreads();
   }
-  if (threadIdx.x == 0) {
-    sh.best = sh.lists[0][n_top - 1];
-    sh.count = 0;
+}
+
+// A warp's running list: `best` in falling order over the lanes, `n` candidates waiting.
+struct Top {
+  u64 best = 0ull, last = 0ull;  // last: the n_top-th, the same in all lanes
+  int n = 0;
+};
+// The first 32 waiting candidates (or all n < 32) into the list.
+Q4G_DEV void take_in(Top& t, u64* wait, int lane, int n_top) {
+  __syncwarp();
+  const u64 k = lane < t.n ? wait[lane] : 0ull, rest = 32 + lane < t.n ? wait[32 + lane] : 0ull;
+  t.best = merge_lists(t.best, sort_desc(k, lane), lane);
+  __syncwarp();
+  t.n = t.n > 32 ? t.n - 32 : 0;
+  if (lane < t.n) wait[lane] = rest;
+  __syncwarp();
+  t.last = shfl_key(t.best, n_top - 1);
+}
+
+// Four logits from index 4 v - skew on, -inf for what lies outside [0, vocab).
+Q4G_DEV float4 load_piece(const float* x, int v, int v_end, int skew, int vocab) {
+  const int first = 4 * v - skew;
+  if (v < v_end && first >= 0 && first + 3 < vocab) {
+    const uint4 u = ld_stream_u4(x + first);
+    return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
   }
+  auto one = [&](int i) { return v < v_end && i >= 0 && i < vocab ? __ldg(x + i) : -INFINITY; };
+  return make_float4(one(first), one(first + 1), one(first + 2), one(first + 3));
+}
+
+template <int THREADS>
+Q4G_DEV void load_tile(const float* x, int v0, int v_end, int skew, int vocab, float (&f)[4 * kVecs]) {
+#pragma unroll
+  for (int k = 0; k < kVecs; ++k) {
+    const float4 u = load_piece(x, v0 + k * THREADS + threadIdx.x, v_end, skew, vocab);
+    f[4 * k] = u.x, f[4 * k + 1] = u.y, f[4 * k + 2] = u.z, f[4 * k + 3] = u.w;
+  }
+}
+
+// The CTA's 32 best logits (n_top of them for certain) into sh.lists[0]; `mine`: the
+// largest of this thread's logits.
+template <int THREADS>
+Q4G_DEV void find_top(LpShared<THREADS>& sh, const float* x, int v_begin, int v_end, int skew, int vocab, float mine,
+                      int n_top) {
+  constexpr int kWarps = THREADS / 32;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t key = (uint32_t)(make_key(mine, 0) >> 32);
+  if (tid == 0) sh.n_hits = 0;
+  merge_warps(sh.maxima, sort_desc(key, lane));
+  const uint32_t lowest = sh.maxima[0][n_top - 1];
+  if (key >= lowest) sh.hits[atomicAdd(&sh.n_hits, 1)] = (uint16_t)tid;
   __syncthreads();
+  // every piece of the threads found, a warp a thread, a lane a piece
+  const float thr = key_value((u64)lowest << 32);
+  const int pieces = (v_end - v_begin + THREADS - 1) / THREADS, n_hits = sh.n_hits;
+  Top top;
+  for (int h = warp; h < n_hits; h += kWarps) {
+    const int v_hit = v_begin + sh.hits[h];
+    for (int q0 = 0; q0 < pieces; q0 += 64) {
+      float4 f[2];
+#pragma unroll
+      for (int b = 0; b < 2; ++b)
+        f[b] = load_piece(x, q0 + 32 * b + lane < pieces ? v_hit + (q0 + 32 * b + lane) * THREADS : v_end, v_end, skew,
+                          vocab);
+#pragma unroll
+      for (int b = 0; b < 2; ++b) {
+        const int v = v_hit + (q0 + 32 * b + lane) * THREADS;
+        const float e[4] = {f[b].x, f[b].y, f[b].z, f[b].w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if (__any_sync(0xffffffffu, e[j] >= thr)) {
+            const int i = 4 * v - skew + j;
+            const u64 k = make_key(e[j], i);
+            // inside the row, and not behind what this warp has
+            const bool in = e[j] >= thr && q0 + 32 * b + lane < pieces && v < v_end && i >= 0 && i < vocab && k > top.last;
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            if (in) sh.wait[warp][top.n + __popc(all & ((1u << lane) - 1))] = k;
+            top.n += __popc(all);
+            if (top.n >= 32) take_in(top, sh.wait[warp], lane, n_top);
+          }
+        }
+      }
+    }
+  }
+  if (top.n > 0) take_in(top, sh.wait[warp], lane, n_top);
+  merge_warps(sh.lists, top.best);
 }
 
 // A cluster of gridDim.x CTAs per row, gridDim.y rows. TOP: alternatives are wanted.
-template <bool TOP>
-__global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams p) {
-  extern __shared__ __align__(16) unsigned char smem_raw[];
-  LpShared& sh = *reinterpret_cast<LpShared*>(smem_raw);
-  u64* const buf = reinterpret_cast<u64*>(smem_raw + ((sizeof(LpShared) + 15) & ~15ul));
+template <bool TOP, int THREADS>
+__global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_kernel(const LogprobParams p) {
+  constexpr int kWarps = THREADS / 32;
+  __shared__ LpShared<THREADS> sh;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;
   const float* x = p.logits + (int64_t)row * p.row_stride;
@@ -163,44 +241,28 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   const int per = (n_vec + ranks - 1) / ranks;
   const int v_end = min(n_vec, (rank + 1) * per);
   const float c = 1.4426950408889634f / p.temperature;
+  float next[4 * kVecs];  // the tile after the one at work: its loads are in flight meanwhile
+  load_tile<THREADS>(x, rank * per, v_end, skew, p.vocab, next);
   const float x_target = rank == 0 && tid == 0 && p.targets && p.targets[row] >= 0 && p.targets[row] < p.vocab
                              ? x[p.targets[row]]
                              : __uint_as_float(0x7fc00000u);
-  if (TOP) {
-    if (tid == 0) sh.best = 0ull, sh.count = 0;
-    __syncthreads();
-  }
 
   Stat st = {kLowest, 0.f, 0.f};
-  bool held = false;
-  for (int v0 = rank * per; v0 < v_end; v0 += kLpThreads * kVecs) {
+  float largest = -INFINITY;
+  for (int v0 = rank * per; v0 < v_end; v0 += THREADS * kVecs) {
     float f[4 * kVecs];
-    int first[kVecs];  // index of each piece's first logit
 #pragma unroll
-    for (int k = 0; k < kVecs; ++k) {
-      const int v = v0 + k * kLpThreads + tid;
-      first[k] = 4 * v - skew;
-      if (v < v_end && first[k] >= 0 && first[k] + 3 < p.vocab) {
-        const uint4 u = ld_stream_u4(x + first[k]);
-        f[4 * k] = __uint_as_float(u.x), f[4 * k + 1] = __uint_as_float(u.y);
-        f[4 * k + 2] = __uint_as_float(u.z), f[4 * k + 3] = __uint_as_float(u.w);
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int i = first[k] + j;
-          f[4 * k + j] = v < v_end && i >= 0 && i < p.vocab ? __ldg(x + i) : -INFINITY;
-        }
-      }
-    }
+    for (int k = 0; k < 4 * kVecs; ++k) f[k] = next[k];
+    if (v0 + THREADS * kVecs < v_end) load_tile<THREADS>(x, v0 + THREADS * kVecs, v_end, skew, p.vocab, next);
     float mx = f[0];
 #pragma unroll
     for (int k = 1; k < 4 * kVecs; ++k) mx = fmaxf(mx, f[k]);
-    {
-      const float m = fmaxf(st.m, mx);
-      const float d0 = fmaxf((st.m - m) * c, kFar), w = ex2(d0);
+    largest = fmaxf(largest, mx);
+    if (mx > st.m) {
+      const float d0 = fmaxf((st.m - mx) * c, kFar), w = ex2(d0);
       st.e = (st.e + d0 * st.l) * w;
       st.l *= w;
-      st.m = m;
+      st.m = mx;
     }
 #pragma unroll
     for (int k = 0; k < 4 * kVecs; ++k) {
@@ -209,50 +271,8 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
       st.l += w;
       st.e = fmaf(w, fmaxf(d, kFar), st.e);
     }
-    if (TOP) {
-      // the lowest logit that may still belong to the answer
-      uint32_t thr;
-      u64 best = 0ull;
-      if (!held) {
-        // a warp's n_top-th largest lane maximum is reached by n_top logits; the
-        // highest of the warps' counts
-        const uint32_t mine = (uint32_t)(make_key(mx, 0) >> 32);
-        const uint32_t s = __shfl_sync(0xffffffffu, sort_desc(mine, lane), p.n_top - 1);
-        if (lane == 0) sh.warp_thr[warp] = s;
-        __syncthreads();
-        thr = 0u;
-#pragma unroll
-        for (int k = 0; k < kLpWarps; ++k) thr = max(thr, sh.warp_thr[k]);
-      } else {
-        best = sh.best;
-        thr = (uint32_t)(best >> 32);
-      }
-      if ((uint32_t)(make_key(mx, 0) >> 32) >= thr) {
-#pragma unroll
-        for (int k = 0; k < 4 * kVecs; ++k) {
-          const int i = first[k >> 2] + (k & 3);
-          const int v = v0 + (k >> 2) * kLpThreads + tid;
-          const u64 key = make_key(f[k], i);
-          if (v < v_end && i >= 0 && i < p.vocab && (uint32_t)(key >> 32) >= thr && key > best) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < kBuf) buf[at] = key;
-          }
-        }
-      }
-      __syncthreads();
-      const int count = sh.count;
-      __syncthreads();
-      if (!held || count > kKeep) {
-        compact(sh, buf, min(count, kBuf), held, p.n_top);
-        held = true;
-      }
-    }
   }
-  if (TOP) {
-    const int count = sh.count;
-    __syncthreads();
-    if (count > 0 || !held) compact(sh, buf, min(count, kBuf), held, p.n_top);
-  }
+  if (TOP) find_top(sh, x, rank * per, v_end, skew, p.vocab, largest, p.n_top);
 
   // the CTA's statistics: lanes, then warps, in a fixed order
 #pragma unroll
@@ -263,35 +283,38 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   }
   if (lane == 0) sh.warp_stat[warp] = st;
   __syncthreads();
-  if (tid == 0) {
-    st = sh.warp_stat[0];
-    for (int k = 1; k < kLpWarps; ++k) st = stat_join(st, sh.warp_stat[k], c);
-    sh.stat = st;
+  if (warp == 0) {
+    st = lane < kWarps ? sh.warp_stat[lane] : Stat{kLowest, 0.f, 0.f};
+#pragma unroll
+    for (int o = kWarps / 2; o > 0; o >>= 1) {
+      Stat b = {__shfl_xor_sync(0xffffffffu, st.m, o), __shfl_xor_sync(0xffffffffu, st.l, o),
+                __shfl_xor_sync(0xffffffffu, st.e, o)};
+      st = stat_join(st, b, c);
+    }
+    if (lane == 0) sh.stat = st;
   }
   if (ranks > 1) {
     cluster_sync();  // every rank's list and statistics are written
     if (rank == 0) {
-      if (TOP) {
-        u64 best = warp < ranks ? ld_peer_u64(peer_addr(&sh.lists[0][lane], warp)) : 0ull;
-        __syncthreads();  // lists[0] of this CTA is read before lists[] is reused
-        sh.lists[warp][lane] = best;
-        __syncthreads();
+      u64 best = 0ull;
+      if (TOP && warp < ranks) best = ld_peer_u64(peer_addr(&sh.lists[0][lane], warp));
+      if (warp == 0) {  // a lane per rank
+        Stat b = {kLowest, 0.f, 0.f};
+        if (lane < ranks)
+          b = {ld_peer_f32(peer_addr(&sh.stat.m, lane)), ld_peer_f32(peer_addr(&sh.stat.l, lane)),
+               ld_peer_f32(peer_addr(&sh.stat.e, lane))};
 #pragma unroll
-        for (int s = 1; s < kLpWarps; s <<= 1) {
-          if (warp % (2 * s) == 0) {
-            best = merge_lists(best, sh.lists[warp + s][lane], lane);
-            sh.lists[warp][lane] = best;
-          }
-          __syncthreads();
+        for (int o = kMaxCluster / 2; o > 0; o >>= 1) {
+          const Stat a = {__shfl_xor_sync(0xffffffffu, b.m, o), __shfl_xor_sync(0xffffffffu, b.l, o),
+                          __shfl_xor_sync(0xffffffffu, b.e, o)};
+          b = stat_join(b, a, c);
         }
+        __syncwarp();
+        if (lane == 0) sh.stat = b;
       }
-      if (tid == 0) {
-        for (int r = 1; r < ranks; ++r) {
-          const Stat b = {ld_peer_f32(peer_addr(&sh.stat.m, r)), ld_peer_f32(peer_addr(&sh.stat.l, r)),
-                          ld_peer_f32(peer_addr(&sh.stat.e, r))};
-          st = stat_join(st, b, c);
-        }
-        sh.stat = st;
+      if (TOP) {
+        __syncthreads();  // lists[0] of this CTA is read before lists[] is reused
+        merge_warps(sh.lists, best);
       }
     }
     cluster_sync();  // no rank leaves while rank 0 reads its shared memory
@@ -309,7 +332,7 @@ __global__ void __launch_bounds__(kLpThreads) logprob_kernel(const LogprobParams
   if (TOP && lane < p.n_top) {
     const u64 k = sh.lists[0][lane];
     const int64_t at = (int64_t)row * p.n_top + lane;
-    // a NaN among the logits may leave fewer than n_top candidates: stay inside the row
+    // NaNs among the logits may leave fewer than n_top candidates: stay inside the row
     if (p.top_ids) p.top_ids[at] = k ? key_index(k) : 0;
     if (p.top_logprobs)
       p.top_logprobs[at] = (k ? key_value(k) - all.m : __uint_as_float(0x7fc00000u)) / p.temperature - ln;
@@ -323,28 +346,35 @@ q4g_status bad(q4g_status s, const char* msg) {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-template <bool TOP>
+template <bool TOP, int THREADS>
 cudaError_t launch_t(const LogprobParams& p, int ranks, cudaStream_t st) {
   cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(kLpThreads);
+  cfg.blockDim = dim3(THREADS);
   cfg.gridDim = dim3(ranks, p.rows);
-  cfg.dynamicSmemBytes = ((sizeof(LpShared) + 15) & ~15ul) + (TOP ? sizeof(u64) * kBuf : 0);
   cfg.stream = st;
   cudaLaunchAttribute at{};
   at.id = cudaLaunchAttributeClusterDimension;
   at.val.clusterDim = {(unsigned)ranks, 1, 1};
   cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<TOP>, p);
+  cfg.numAttrs = ranks > 1 ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, logprob_kernel<TOP, THREADS>, p);
+}
+
+template <int THREADS>
+cudaError_t launch_rows(const LogprobParams& p, int ranks, cudaStream_t st) {
+  return p.n_top ? launch_t<true, THREADS>(p, ranks, st) : launch_t<false, THREADS>(p, ranks, st);
 }
 
 }  // namespace
 
 cudaError_t q4g::launch_logprobs(const LogprobParams& p, cudaStream_t st) {
-  // CTAs per row: enough for about six CTAs on every SM, but at least a tile for each
-  const int64_t tiles = ((int64_t)p.vocab + kTile - 1) / kTile;
+  // Few rows: clusters of CTAs of 1024 threads, an SM each, so that a row's loads are all
+  // in flight within a few tiles. Many: CTAs of 256 threads, about six on every SM.
+  const int sms = device_sm_count();
+  const bool large = p.rows * kMaxCluster <= sms && p.vocab > 2 * tile_of(kSmall);
+  const int64_t tiles = ((int64_t)p.vocab + tile_of(large ? kLarge : kSmall) - 1) / tile_of(large ? kLarge : kSmall);
   int ranks = 1;
-  while (ranks < kMaxCluster && (int64_t)p.rows * ranks < 6ll * device_sm_count() && 2 * ranks <= tiles) ranks *= 2;
+  while (ranks < kMaxCluster && (int64_t)p.rows * ranks < (large ? 1 : 6) * (int64_t)sms && 2 * ranks <= tiles) ranks *= 2;
   // the grid's y extent ends at 65535: longer calls go in pieces
   for (int r0 = 0; r0 < p.rows; r0 += 65535) {
     LogprobParams q = p;
@@ -355,7 +385,7 @@ cudaError_t q4g::launch_logprobs(const LogprobParams& p, cudaStream_t st) {
     if (q.entropy) q.entropy += r0;
     if (q.top_ids) q.top_ids += (int64_t)r0 * p.n_top;
     if (q.top_logprobs) q.top_logprobs += (int64_t)r0 * p.n_top;
-    const cudaError_t e = p.n_top ? launch_t<true>(q, ranks, st) : launch_t<false>(q, ranks, st);
+    const cudaError_t e = large ? launch_rows<kLarge>(q, ranks, st) : launch_rows<kSmall>(q, ranks, st);
     if (e != cudaSuccess) return e;
   }
   return cudaSuccess;
