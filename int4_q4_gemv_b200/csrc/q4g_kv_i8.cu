@@ -3,9 +3,10 @@
 // scale = amax / 127 and codes rint(x / scale), the format the decode step writes
 // (kv_quantize_row_warp) and the _i8 attention kernels read.
 //
-// Bound by HBM: 2 + 1 bytes per element and 4 per row, nothing read twice. A warp
-// holds a whole row in registers (8 or 16 values per lane, 16-byte loads), so the
-// amax needs no second pass; the row goes out as one 8- or 16-byte store per lane.
+// Bound by HBM: 2 + 1 bytes per element and 4 per row, nothing read twice. A lane holds
+// 16 values of a row, 32 lanes (hd 512) or 16 (hd 256, two rows a warp) the row, so the
+// amax needs no second pass. (8 values
+// a lane at hd 256 ran at 3.6 TB/s: what a row costs beside its bytes came twice as often.)
 #include "../../include/q4g.h"
 #include "q4g_common.cuh"
 #include "q4g_internal.h"
@@ -48,10 +49,10 @@ Q4G_DEV int64_t cache_row(const KvCopyParams& p, int t, int h) {
 // issue slots than the row's bytes cost HBM time. |v| / s rounds to 127 at most.
 // Adding 1.5 * 2^23 rounds to the nearest integer, ties to even, in the low bits.
 template <int E>
-Q4G_DEV void quantize(float (&v)[E], float s, bool finite, uint32_t (&w)[E / 4]) {
+Q4G_DEV void quantize(float (&v)[E], float s, bool no_nan, uint32_t (&w)[E / 4]) {
   constexpr float kMagic = 12582912.0f;
   const bool huge = s > 3.0e38f;  // an infinite value in the row: every code 0
-  if (!finite || huge) {
+  if (!no_nan || huge) {
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = huge || !(fabsf(v[e]) < 1e6f) ? 0.f : v[e];
   }
@@ -71,85 +72,106 @@ Q4G_DEV void quantize(float (&v)[E], float s, bool finite, uint32_t (&w)[E / 4])
   }
 }
 
-template <int E>
-Q4G_DEV void load_row(const __half* p, uint4 (&r)[E / 8]) {
-#pragma unroll
-  for (int k = 0; k < E / 8; ++k) r[k] = ld_stream_u4(p + 8 * k);
+constexpr int E = 16;  // values of a row per lane
+template <int HD>
+constexpr int kRowLanes = HD / E;
+template <int HD>
+constexpr int kRowsAtOnce = kKvThreads / kRowLanes<HD>;  // rows of a CTA at a time
+
+// A lane's values are 8 of the row's first half and 8 of its second, so that the lanes of a
+// 16-byte load or store (8 bytes of codes) are neighbours.
+template <int HD>
+Q4G_DEV void load_row(const __half* p, uint4 (&r)[2]) {
+  r[0] = ld_stream_u4(p);
+  r[1] = ld_stream_u4(p + HD / 2);
 }
 
+// Both kernels load the next row before they work on this one.
 template <int HD>
 __global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCopyParams p) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x % kRowLanes<HD>;
   const bool is_v = blockIdx.y != 0;
-  __half* const rows = is_v ? p.v : p.k;
-  int8_t* const codes = is_v ? p.v_codes : p.k_codes;
+  const __half* const rows = (is_v ? p.v : p.k) + lane * 8;
+  int8_t* const codes = (is_v ? p.v_codes : p.k_codes) + lane * 8;
   float* const scales = is_v ? p.v_scales : p.k_scales;
-  const int total = p.n * p.n_kv;
-  const int step = gridDim.x * (kKvThreads / 32);
-  for (int64_t i = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
-    const int t = (int)i / p.n_kv, h = (int)i - t * p.n_kv;
-    const int64_t row = cache_row(p, t, h);
-    if (row < 0) continue;
-    uint4 raw[E / 8];
-    load_row<E>(rows + t * p.row_stride + h * HD + lane * E, raw);
-    float v[E], amax = 0.f, odd = 0.f;
+  const int total = p.n * p.n_kv, step = gridDim.x * kRowsAtOnce<HD>;
+  int i = blockIdx.x * kRowsAtOnce<HD> + threadIdx.x / kRowLanes<HD>;
+  // the lanes of a warp stay together: a row past the end is no row
+  uint4 next[2] = {};
+  int64_t next_row = -1;
+  auto load = [&]() {
+    next_row = -1;
+    if (i >= total) return;
+    const int t = i / p.n_kv, h = i - t * p.n_kv;
+    load_row<HD>(rows + t * p.row_stride + h * HD, next);
+    next_row = cache_row(p, t, h);
+  };
+  load();
+  for (int turns = (total + step - 1) / step; turns > 0; --turns) {
+    const uint4 raw[2] = {next[0], next[1]};
+    const int64_t row = next_row;
+    i = i < total - step ? i + step : total;
+    load();
+    const uint32_t u[8] = {raw[0].x, raw[0].y, raw[0].z, raw[0].w, raw[1].x, raw[1].y, raw[1].z, raw[1].w};
+    float v[E];
+    __half2 most = __floats2half2_rn(0.f, 0.f), any = most;  // `any` keeps a NaN, `most` does not
 #pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
-      const uint32_t u[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-        v[8 * k + 2 * j] = f.x;
-        v[8 * k + 2 * j + 1] = f.y;
-        amax = fmaxf(amax, fmaxf(fabsf(f.x), fabsf(f.y)));
-        odd = fmaf(f.x, 0.f, fmaf(f.y, 0.f, odd));  // a NaN or an infinity makes it NaN
-      }
+    for (int k = 0; k < 8; ++k) {
+      const __half2 x = *reinterpret_cast<const __half2*>(&u[k]);
+      const float2 f = __half22float2(x);
+      v[2 * k] = f.x;
+      v[2 * k + 1] = f.y;
+      most = __hmax2(most, __habs2(x));
+      any = __hmax2_nan(any, __habs2(x));
     }
-    const float s = __fdiv_rn(warp_max(amax), 127.0f);
+    float amax = fmaxf(__low2float(most), __high2float(most));
+#pragma unroll
+    for (int o = kRowLanes<HD> / 2; o > 0; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+    const float s = __fdiv_rn(amax, 127.0f);
     uint32_t w[E / 4];
-    quantize<E>(v, s, odd == 0.f, w);
-    int8_t* out = codes + row * HD + lane * E;
-    if constexpr (E == 16) {
-      *reinterpret_cast<uint4*>(out) = make_uint4(w[0], w[1], w[2], w[3]);
-    } else {
-      *reinterpret_cast<uint2*>(out) = make_uint2(w[0], w[1]);
+    quantize<E>(v, s, !(__hisnan(__low2half(any)) || __hisnan(__high2half(any))), w);
+    if (row >= 0) {
+      *reinterpret_cast<uint2*>(codes + row * HD) = make_uint2(w[0], w[1]);
+      *reinterpret_cast<uint2*>(codes + row * HD + HD / 2) = make_uint2(w[2], w[3]);
+      if (lane == 0) scales[row] = s;
     }
-    if (lane == 0) scales[row] = s;
   }
 }
 
 template <int HD>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCopyParams p) {
-  constexpr int E = HD / 32;
-  const int lane = threadIdx.x & 31;
+  const int lane = threadIdx.x % kRowLanes<HD>;
   const bool is_v = blockIdx.y != 0;
-  __half* const rows = is_v ? p.v : p.k;
-  int8_t* const codes = is_v ? p.v_codes : p.k_codes;
-  float* const scales = is_v ? p.v_scales : p.k_scales;
-  const int total = p.n * p.n_kv;
-  const int step = gridDim.x * (kKvThreads / 32);
-  for (int64_t i = blockIdx.x * (kKvThreads / 32) + (threadIdx.x >> 5); i < total; i += step) {
-    const int t = (int)i / p.n_kv, h = (int)i - t * p.n_kv;
+  __half* const rows = (is_v ? p.v : p.k) + lane * 8;
+  const int8_t* const codes = (is_v ? p.v_codes : p.k_codes) + lane * 8;
+  const float* const scales = is_v ? p.v_scales : p.k_scales;
+  const int total = p.n * p.n_kv, step = gridDim.x * kRowsAtOnce<HD>;
+  int i = blockIdx.x * kRowsAtOnce<HD> + threadIdx.x / kRowLanes<HD>;
+  uint2 next[2] = {};
+  float next_s = 0.f;
+  __half* next_out = nullptr;
+  auto load = [&]() {
+    if (i >= total) return;
+    const int t = i / p.n_kv, h = i - t * p.n_kv;
+    next_out = rows + t * p.row_stride + h * HD;
     const int64_t row = cache_row(p, t, h);
-    uint32_t w[E / 4];
-    float s = 0.f;
-#pragma unroll
-    for (int k = 0; k < E / 4; ++k) w[k] = 0u;
+    next[0] = next[1] = make_uint2(0u, 0u);  // a slot outside the cache: zeros
+    next_s = 0.f;
     if (row >= 0) {
-      const int8_t* in = codes + row * HD + lane * E;
-      s = __ldg(scales + row);
-      if constexpr (E == 16) {
-        const uint4 u = ld_stream_u4(in);
-        w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-      } else {
-        const uint2 u = __ldg(reinterpret_cast<const uint2*>(in));
-        w[0] = u.x, w[1] = u.y;
-      }
+      next[0] = __ldg(reinterpret_cast<const uint2*>(codes + row * HD));
+      next[1] = __ldg(reinterpret_cast<const uint2*>(codes + row * HD + HD / 2));
+      next_s = __ldg(scales + row);
     }
-    __half* out = rows + t * p.row_stride + h * HD + lane * E;
+  };
+  load();
+  while (i < total) {
+    const uint32_t w[4] = {next[0].x, next[0].y, next[1].x, next[1].y};
+    const float s = next_s;
+    __half* const out = next_out;
+    i = i < total - step ? i + step : total;
+    load();
 #pragma unroll
-    for (int k = 0; k < E / 8; ++k) {
+    for (int k = 0; k < 2; ++k) {
       uint32_t o[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
@@ -157,7 +179,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCopyParams 
         const __half2 h2 = __floats2half2_rn((float)(int8_t)(c & 0xff) * s, (float)(int8_t)((c >> 8) & 0xff) * s);
         o[j] = *reinterpret_cast<const uint32_t*>(&h2);
       }
-      *reinterpret_cast<uint4*>(out + 8 * k) = make_uint4(o[0], o[1], o[2], o[3]);
+      *reinterpret_cast<uint4*>(out + k * (HD / 2)) = make_uint4(o[0], o[1], o[2], o[3]);
     }
   }
 }
@@ -207,10 +229,9 @@ q4g_status check_pointers(const void* k, const void* v, const void* kc, const vo
 }
 
 template <typename K>
-q4g_status launch(K kernel, const KvCopyParams& p, cudaStream_t st) {
-  const int warps = kKvThreads / 32;
-  const int64_t need = ((int64_t)p.n * p.n_kv + warps - 1) / warps;
-  const int64_t cap = 4ll * device_sm_count();
+q4g_status launch(K kernel, int rows_at_once, const KvCopyParams& p, cudaStream_t st) {
+  const int64_t need = ((int64_t)p.n * p.n_kv + rows_at_once - 1) / rows_at_once;
+  const int64_t cap = 12ll * device_sm_count();  // for K and V each
   const dim3 grid((unsigned)(need < cap ? need : cap), 2);
   kernel<<<grid, kKvThreads, 0, st>>>(p);
   const cudaError_t e = cudaGetLastError();
@@ -245,13 +266,15 @@ void ring_slots(KvCopyParams& p, int64_t pos0, int64_t ring) {
 q4g_status run_write(KvCopyParams& p, const uint16_t* k, const uint16_t* v, int32_t hd, cudaStream_t st) {
   p.k = reinterpret_cast<__half*>(const_cast<uint16_t*>(k));
   p.v = reinterpret_cast<__half*>(const_cast<uint16_t*>(v));
-  return hd == 512 ? launch(kv_write_kernel<512>, p, st) : launch(kv_write_kernel<256>, p, st);
+  return hd == 512 ? launch(kv_write_kernel<512>, kRowsAtOnce<512>, p, st)
+                   : launch(kv_write_kernel<256>, kRowsAtOnce<256>, p, st);
 }
 
 q4g_status run_read(KvCopyParams& p, uint16_t* k, uint16_t* v, int32_t hd, cudaStream_t st) {
   p.k = reinterpret_cast<__half*>(k);
   p.v = reinterpret_cast<__half*>(v);
-  return hd == 512 ? launch(kv_read_kernel<512>, p, st) : launch(kv_read_kernel<256>, p, st);
+  return hd == 512 ? launch(kv_read_kernel<512>, kRowsAtOnce<512>, p, st)
+                   : launch(kv_read_kernel<256>, kRowsAtOnce<256>, p, st);
 }
 
 }  // namespace

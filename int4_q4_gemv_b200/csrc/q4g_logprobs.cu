@@ -6,10 +6,12 @@
 // Bound by HBM: 4 bytes per logit, read once. Every thread keeps its own running
 // (m, S, E = sum exp(d) d) and rescales them when its maximum moves; E counts from
 // the maximum, so the entropy is a sum of terms of one sign and cancels nothing.
-// The alternatives cost the pass nothing: it leaves every thread's largest logit, and the
-// n_top best logits of a CTA's part lie with the threads whose largest is at least the
-// n_top-th largest of those (n_top logits reach it). Only these threads' logits, n_top of
-// 256 or 1024 shares, are read again, from L2. (Lists kept up to date while reading, per
+// The alternatives cost the pass nothing: it leaves the largest logit of every share (a
+// thread's logits in an eighth of the CTA's tiles), and the n_top best logits of a CTA's
+// part lie in the shares whose largest is at least the n_top-th largest of those (n_top
+// logits reach it). Only these n_top of some 2000 shares are read again. (Shares of whole
+// threads read 42 MB again for 256 rows with 20 alternatives, 60 us against 50; lists kept
+// up to date while reading, per
 // CTA or per warp, took 98 and 106 us on 256 rows of 262,144 logits with 20 alternatives,
 // 52 and 60 more than without alternatives.)
 // A row is split over the CTAs of one thread-block cluster when there are few rows;
@@ -30,6 +32,7 @@ constexpr int kVecs = 4;           // 16-byte loads per thread and tile
 constexpr int kMaxCluster = 8;     // no more than a CTA's warps: one merges one CTA's list
 constexpr int kSmall = 256, kLarge = 1024;  // threads per CTA
 constexpr int tile_of(int threads) { return threads * kVecs * 4; }  // logits per tile
+constexpr int shares_of(int threads) { return 2048 / threads; }    // of a thread, at most
 
 typedef unsigned long long u64;
 
@@ -110,12 +113,13 @@ Q4G_DEV Stat stat_join(Stat a, Stat b, float c) {
 template <int THREADS>
 struct LpShared {
   u64 lists[THREADS / 32][32];  // the warps' lists while merging; [0] is then the CTA's
-  u64 wait[THREADS / 32][64];   // a warp's candidates until they are 32
+  u64 wait[THREADS / 32][64];   // candidates: the CTA's in a row, or each warp's until they are 32
   Stat warp_stat[THREADS / 32];
   Stat stat;
-  uint32_t maxima[THREADS / 32][32];  // as lists, of the threads' largest logits (keys' high words)
-  uint16_t hits[THREADS];       // threads to read again
-  int n_hits;
+  uint32_t maxima[THREADS / 32][32];  // as lists, of the shares' largest logits (keys' high words)
+  float largest[shares_of(THREADS)][THREADS];
+  uint16_t hits[shares_of(THREADS) * THREADS];  // shares to read again: number * THREADS + thread
+  int n_hits, n_found;
 };
 
 Q4G_DEV u64 ld_peer_u64(uint32_t addr) {
@@ -124,16 +128,16 @@ Q4G_DEV u64 ld_peer_u64(uint32_t addr) {
   return v;
 }
 
-// The warps' lists, each in falling order, into one: the 32 best, in lists[0]. All threads
-// call it; it ends with a barrier.
-template <int WARPS, typename K>
+// The first N warps' lists, each in falling order, into one: the 32 best, in lists[0]. All
+// threads call it; it ends with a barrier.
+template <int N, int WARPS, typename K>
 Q4G_DEV void merge_warps(K (&lists)[WARPS][32], K best) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  lists[warp][lane] = best;
+  if (warp < N) lists[warp][lane] = best;
   __syncthreads();
 #pragma unroll
-  for (int s = 1; s < WARPS; s <<= 1) {
-    if (warp % (2 * s) == 0) {
+  for (int s = 1; s < N; s <<= 1) {
+    if (warp < N && warp % (2 * s) == 0) {
       best = merge_lists(best, lists[warp + s][lane], lane);
       lists[warp][lane] = best;
     }
@@ -178,25 +182,16 @@ Q4G_DEV void load_tile(const float* x, int v0, int v_end, int skew, int vocab, f
   }
 }
 
-// The CTA's 32 best logits (n_top of them for certain) into sh.lists[0]; `mine`: the
-// largest of this thread's logits.
-template <int THREADS>
-Q4G_DEV void find_top(LpShared<THREADS>& sh, const float* x, int v_begin, int v_end, int skew, int vocab, float mine,
-                      int n_top) {
-  constexpr int kWarps = THREADS / 32;
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const uint32_t key = (uint32_t)(make_key(mine, 0) >> 32);
-  if (tid == 0) sh.n_hits = 0;
-  merge_warps(sh.maxima, sort_desc(key, lane));
-  const uint32_t lowest = sh.maxima[0][n_top - 1];
-  if (key >= lowest) sh.hits[atomicAdd(&sh.n_hits, 1)] = (uint16_t)tid;
-  __syncthreads();
-  // every piece of the threads found, a warp a thread, a lane a piece
-  const float thr = key_value((u64)lowest << 32);
-  const int pieces = (v_end - v_begin + THREADS - 1) / THREADS, n_hits = sh.n_hits;
-  Top top;
-  for (int h = warp; h < n_hits; h += kWarps) {
-    const int v_hit = v_begin + sh.hits[h];
+// Every piece of the shares in sh.hits, a warp a share and a lane a piece: take(key, whether
+// the index is inside the row and the logit reaches thr) in converged warps. `per`: pieces
+// of a thread in a share.
+template <int THREADS, typename F>
+Q4G_DEV void read_again(const LpShared<THREADS>& sh, const float* x, int v_begin, int v_end, int per, int skew,
+                        int vocab, float thr, F take) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_hits = sh.n_hits;
+  for (int h = warp; h < n_hits; h += THREADS / 32) {
+    const int share = sh.hits[h] / THREADS, v_hit = v_begin + share * per * THREADS + sh.hits[h] % THREADS;
+    const int pieces = per;
     for (int q0 = 0; q0 < pieces; q0 += 64) {
       float4 f[2];
 #pragma unroll
@@ -211,20 +206,69 @@ Q4G_DEV void find_top(LpShared<THREADS>& sh, const float* x, int v_begin, int v_
         for (int j = 0; j < 4; ++j) {
           if (__any_sync(0xffffffffu, e[j] >= thr)) {
             const int i = 4 * v - skew + j;
-            const u64 k = make_key(e[j], i);
-            // inside the row, and not behind what this warp has
-            const bool in = e[j] >= thr && q0 + 32 * b + lane < pieces && v < v_end && i >= 0 && i < vocab && k > top.last;
-            const uint32_t all = __ballot_sync(0xffffffffu, in);
-            if (in) sh.wait[warp][top.n + __popc(all & ((1u << lane) - 1))] = k;
-            top.n += __popc(all);
-            if (top.n >= 32) take_in(top, sh.wait[warp], lane, n_top);
+            take(make_key(e[j], i), e[j] >= thr && q0 + 32 * b + lane < pieces && v < v_end && i >= 0 && i < vocab);
           }
         }
       }
     }
   }
-  if (top.n > 0) take_in(top, sh.wait[warp], lane, n_top);
-  merge_warps(sh.lists, top.best);
+}
+
+// The CTA's 32 best logits (n_top of them for certain) into sh.lists[0], from the shares'
+// largest in sh.largest (each thread's own are written). Ends with a barrier.
+template <int THREADS>
+Q4G_DEV void find_top(LpShared<THREADS>& sh, const float* x, int v_begin, int v_end, int shares, int per, int skew,
+                      int vocab, int n_top) {
+  constexpr int kWarps = THREADS / 32, kPool = kWarps * 64;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) sh.n_hits = sh.n_found = 0;
+  uint32_t best = 0u;
+  for (int c = 0; c < shares; ++c) {
+    const uint32_t k = sort_desc((uint32_t)(make_key(sh.largest[c][tid], 0) >> 32), lane);
+    best = c == 0 ? k : merge_lists(best, k, lane);
+  }
+  merge_warps<kWarps>(sh.maxima, best);
+  const uint32_t lowest = sh.maxima[0][n_top - 1];
+  for (int c = 0; c < shares; ++c)
+    if ((uint32_t)(make_key(sh.largest[c][tid], 0) >> 32) >= lowest)
+      sh.hits[atomicAdd(&sh.n_hits, 1)] = (uint16_t)(c * THREADS + tid);
+  __syncthreads();
+  // all that reaches the threshold in one row, as far as there is room: usually a few more
+  // than n_top, which one warp sorts
+  const float thr = key_value((u64)lowest << 32);
+  u64* const pool = &sh.wait[0][0];
+  read_again<THREADS>(sh, x, v_begin, v_end, per, skew, vocab, thr, [&](u64 k, bool in) {
+    const uint32_t all = __ballot_sync(0xffffffffu, in);
+    int at = 0;
+    if (lane == 0) at = atomicAdd(&sh.n_found, __popc(all));
+    at = __shfl_sync(0xffffffffu, at, 0) + __popc(all & ((1u << lane) - 1));
+    if (in && at < kPool) pool[at] = k;
+  });
+  __syncthreads();
+  const int found = sh.n_found;
+  Top top;
+  if (found <= kPool) {
+    const int n = found <= 96 ? 1 : kWarps;  // warps at work
+    if (warp < n)
+      for (int b = warp * 32; b < found; b += 32 * n)
+        top.best = merge_lists(top.best, sort_desc(b + lane < found ? pool[b + lane] : 0ull, lane), lane);
+    if (n == 1) {
+      if (warp == 0) sh.lists[0][lane] = top.best;
+      __syncthreads();
+      return;
+    }
+  } else {  // many equal logits, or all the large ones with few threads: list by list
+    __syncthreads();  // the pool is each warp's own from here on
+    read_again<THREADS>(sh, x, v_begin, v_end, per, skew, vocab, thr, [&](u64 k, bool reaches) {
+      const bool in = reaches && k > top.last;
+      const uint32_t all = __ballot_sync(0xffffffffu, in);
+      if (in) sh.wait[warp][top.n + __popc(all & ((1u << lane) - 1))] = k;
+      top.n += __popc(all);
+      if (top.n >= 32) take_in(top, sh.wait[warp], lane, n_top);
+    });
+    if (top.n > 0) take_in(top, sh.wait[warp], lane, n_top);
+  }
+  merge_warps<kWarps>(sh.lists, top.best);
 }
 
 // A cluster of gridDim.x CTAs per row, gridDim.y rows. TOP: alternatives are wanted.
@@ -248,7 +292,12 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
                              : __uint_as_float(0x7fc00000u);
 
   Stat st = {kLowest, 0.f, 0.f};
-  float largest = -INFINITY;
+  float largest = -INFINITY;  // of the share at work
+  const int tiles = max((v_end - rank * per + THREADS * kVecs - 1) / (THREADS * kVecs), 1);
+  // at least 8 tiles: more shares cost more sorting than they save reading (64 rows of
+  // 262,144 logits, 8 tiles a CTA: 18.4 us as one share, 23.8 us as eight)
+  const int share_tiles = max((tiles + shares_of(THREADS) - 1) / shares_of(THREADS), 8);
+  int share = 0, left = share_tiles;
   for (int v0 = rank * per; v0 < v_end; v0 += THREADS * kVecs) {
     float f[4 * kVecs];
 #pragma unroll
@@ -257,7 +306,14 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
     float mx = f[0];
 #pragma unroll
     for (int k = 1; k < 4 * kVecs; ++k) mx = fmaxf(mx, f[k]);
-    largest = fmaxf(largest, mx);
+    if (TOP) {
+      largest = fmaxf(largest, mx);
+      if (--left == 0) {
+        sh.largest[share++][tid] = largest;
+        left = share_tiles;
+        largest = -INFINITY;
+      }
+    }
     if (mx > st.m) {
       const float d0 = fmaxf((st.m - mx) * c, kFar), w = ex2(d0);
       st.e = (st.e + d0 * st.l) * w;
@@ -272,7 +328,10 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
       st.e = fmaf(w, fmaxf(d, kFar), st.e);
     }
   }
-  if (TOP) find_top(sh, x, rank * per, v_end, skew, p.vocab, largest, p.n_top);
+  if (TOP) {
+    if (left < share_tiles || share == 0) sh.largest[share++][tid] = largest;
+    find_top(sh, x, rank * per, v_end, share, share_tiles * kVecs, skew, p.vocab, p.n_top);
+  }
 
   // the CTA's statistics: lanes, then warps, in a fixed order
 #pragma unroll
@@ -314,7 +373,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
       }
       if (TOP) {
         __syncthreads();  // lists[0] of this CTA is read before lists[] is reused
-        merge_warps(sh.lists, best);
+        merge_warps<kMaxCluster>(sh.lists, best);
       }
     }
     cluster_sync();  // no rank leaves while rank 0 reads its shared memory
@@ -369,12 +428,16 @@ cudaError_t launch_rows(const LogprobParams& p, int ranks, cudaStream_t st) {
 
 cudaError_t q4g::launch_logprobs(const LogprobParams& p, cudaStream_t st) {
   // Few rows: clusters of CTAs of 1024 threads, an SM each, so that a row's loads are all
-  // in flight within a few tiles. Many: CTAs of 256 threads, about six on every SM.
+  // in flight within a few tiles (three quarters of the SMs: more clusters do not fit on the
+  // GPU at once, 16 rows as 16 clusters of 8 took 22 us, as clusters of 4 they take 12). Many:
+  // CTAs of 256 threads, four on every SM at most, the number that fits:
+  // one wave, 42 us for 256 rows of 262,144 logits against 47 with up to six.
   const int sms = device_sm_count();
-  const bool large = p.rows * kMaxCluster <= sms && p.vocab > 2 * tile_of(kSmall);
+  const bool large = (int64_t)p.rows * kMaxCluster <= sms && p.vocab > 2 * tile_of(kSmall);
   const int64_t tiles = ((int64_t)p.vocab + tile_of(large ? kLarge : kSmall) - 1) / tile_of(large ? kLarge : kSmall);
+  const int64_t most = large ? sms * 3 / 4 : 4 * sms;
   int ranks = 1;
-  while (ranks < kMaxCluster && (int64_t)p.rows * ranks < (large ? 1 : 6) * (int64_t)sms && 2 * ranks <= tiles) ranks *= 2;
+  while (ranks < kMaxCluster && 2 * p.rows * (int64_t)ranks <= most && 2 * ranks <= tiles) ranks *= 2;
   // the grid's y extent ends at 65535: longer calls go in pieces
   for (int r0 = 0; r0 < p.rows; r0 += 65535) {
     LogprobParams q = p;
