@@ -88,7 +88,7 @@ Q4G_DEV void load_row(const __half* p, uint4 (&r)[2]) {
 
 // Both kernels load the next row before they work on this one.
 template <int HD>
-__global__ void __launch_bounds__(kKvThreads) kv_write_kernel(const KvCopyParams p) {
+__global__ void __launch_bounds__(kKvThreads, 5) kv_write_kernel(const KvCopyParams p) {
   const int lane = threadIdx.x % kRowLanes<HD>;
   const bool is_v = blockIdx.y != 0;
   const __half* const rows = (is_v ? p.v : p.k) + lane * 8;
