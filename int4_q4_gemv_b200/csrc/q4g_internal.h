@@ -189,6 +189,26 @@ struct StepParams {
 cudaError_t launch_step_init(const StepParams& p, cudaStream_t st);
 
 int device_sm_count();
+// Launch with programmatic stream serialization: the kernel may start while the one before
+// it in the stream ends, so it calls pdl_wait() before it touches global memory. With
+// cluster_x > 1 the grid's x extent is one cluster.
+template <typename... P, typename... A>
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster_x,
+                       A... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute at[2]{};
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim = {(unsigned)cluster_x, 1, 1};
+  cfg.attrs = at;
+  cfg.numAttrs = cluster_x > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
 // Whether p is device memory (or managed memory) of the current device.
 bool on_current_device(const void* p);
 

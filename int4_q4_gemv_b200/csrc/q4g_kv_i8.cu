@@ -89,6 +89,8 @@ Q4G_DEV void load_row(const __half* p, uint4 (&r)[2]) {
 // Both kernels load the next row before they work on this one.
 template <int HD>
 __global__ void __launch_bounds__(kKvThreads, 5) kv_write_kernel(const KvCopyParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x % kRowLanes<HD>;
   const bool is_v = blockIdx.y != 0;
   const __half* const rows = (is_v ? p.v : p.k) + lane * 8;
@@ -140,6 +142,8 @@ __global__ void __launch_bounds__(kKvThreads, 5) kv_write_kernel(const KvCopyPar
 
 template <int HD>
 __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCopyParams p) {
+  pdl_launch_dependents();
+  pdl_wait();
   const int lane = threadIdx.x % kRowLanes<HD>;
   const bool is_v = blockIdx.y != 0;
   __half* const rows = (is_v ? p.v : p.k) + lane * 8;
@@ -233,8 +237,7 @@ q4g_status launch(K kernel, int rows_at_once, const KvCopyParams& p, cudaStream_
   const int64_t need = ((int64_t)p.n * p.n_kv + rows_at_once - 1) / rows_at_once;
   const int64_t cap = 12ll * device_sm_count();  // for K and V each
   const dim3 grid((unsigned)(need < cap ? need : cap), 2);
-  kernel<<<grid, kKvThreads, 0, st>>>(p);
-  const cudaError_t e = cudaGetLastError();
+  const cudaError_t e = launch_pdl(kernel, grid, kKvThreads, 0, st, 1, p);
   return e == cudaSuccess ? Q4G_OK : bad(Q4G_ECUDA, cudaGetErrorString(e));
 }
 

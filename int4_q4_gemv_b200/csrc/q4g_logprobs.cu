@@ -276,6 +276,7 @@ template <bool TOP, int THREADS>
 __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_kernel(const LogprobParams p) {
   constexpr int kWarps = THREADS / 32;
   __shared__ LpShared<THREADS> sh;
+  pdl_wait();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = blockIdx.y, rank = blockIdx.x, ranks = gridDim.x;
   const float* x = p.logits + (int64_t)row * p.row_stride;
@@ -328,6 +329,8 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
       st.e = fmaf(w, fmaxf(d, kFar), st.e);
     }
   }
+  // not earlier: the next kernel's CTAs would gather on the SMs that finish first
+  pdl_launch_dependents();
   if (TOP) {
     if (left < share_tiles || share == 0) sh.largest[share++][tid] = largest;
     find_top(sh, x, rank * per, v_end, share, share_tiles * kVecs, skew, p.vocab, p.n_top);
@@ -405,23 +408,11 @@ q4g_status bad(q4g_status s, const char* msg) {
 
 bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
-template <bool TOP, int THREADS>
-cudaError_t launch_t(const LogprobParams& p, int ranks, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.blockDim = dim3(THREADS);
-  cfg.gridDim = dim3(ranks, p.rows);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeClusterDimension;
-  at.val.clusterDim = {(unsigned)ranks, 1, 1};
-  cfg.attrs = &at;
-  cfg.numAttrs = ranks > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, logprob_kernel<TOP, THREADS>, p);
-}
-
 template <int THREADS>
 cudaError_t launch_rows(const LogprobParams& p, int ranks, cudaStream_t st) {
-  return p.n_top ? launch_t<true, THREADS>(p, ranks, st) : launch_t<false, THREADS>(p, ranks, st);
+  const dim3 grid(ranks, p.rows);
+  return p.n_top ? launch_pdl(logprob_kernel<true, THREADS>, grid, THREADS, 0, st, ranks, p)
+                 : launch_pdl(logprob_kernel<false, THREADS>, grid, THREADS, 0, st, ranks, p);
 }
 
 }  // namespace

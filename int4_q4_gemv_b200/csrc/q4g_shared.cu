@@ -272,15 +272,17 @@ struct State {
   float factor[kGroupRows];
   Segment seg[kQueue];
   uint64_t seg_full[kQueue], seg_empty[kQueue];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_free, o_free, drain;
+  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_free, o_part[4], o_free, drain;
   int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
+  int32_t clean_at;  // the ring stage of the first V part to clear
   volatile int abort;
 };
 template <int HD, bool I8>
 struct RingState : State {
   uint64_t full[Plan<HD, I8>::kStages], empty[Plan<HD, I8>::kStages];
-  uint64_t code_full[Plan<HD, I8>::kCodeStages + 1], code_empty[Plan<HD, I8>::kCodeStages + 1];
+  uint64_t clean_ask[I8 ? 1 : HD / 128], clean_done[I8 ? 1 : HD / 128];  // per V part of a segment's last tile
+  uint64_t code_full[I8 ? Plan<HD, I8>::kCodeStages : 1], code_empty[I8 ? Plan<HD, I8>::kCodeStages : 1];
 };
 
 template <int HD, bool I8>
@@ -357,12 +359,10 @@ struct Scheduler {
   bool more;
   int len;
   uint32_t n = 0;
-  // before the CTA's first barrier: the first own lengths are asked for, and the first prefix
-  // segment comes from the arguments alone
-  Q4G_DEV Scheduler(const SharedParams& p, int lane) : work(p) {
-    len = lane < p.batch ? own_len_of(p, lane) : 0;
-    more = work.next(p, line, s);
-  }
+  // before the CTA's first barrier: the first prefix segment comes from the arguments alone,
+  // then (memory may be read) the first own lengths are asked for
+  Q4G_DEV explicit Scheduler(const SharedParams& p) : work(p) { more = work.next(p, line, s); }
+  Q4G_DEV void ask(const SharedParams& p, int lane) { len = lane < p.batch ? own_len_of(p, lane) : 0; }
   Q4G_DEV bool push(const SharedParams& p, State& sh, int lane) {
     if (n >= kQueue && !wait_warp(sh, p, &sh.seg_empty[n % kQueue], (n / kQueue - 1) & 1)) return false;
     if (lane == 0) {
@@ -459,6 +459,13 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
   }
 }
 
+// What lies behind a sequence's own rows may be anything, and zero times a NaN is not zero:
+// in the last V tile the rows up to the next 16 (those that the products take) are cleared,
+// when the thread that makes the products has seen them arrive, by the softmax warps, which
+// only wait for it then. (Codes are finite, and their scales are masked.)
+template <bool I8>
+Q4G_DEV bool needs_clean(const Segment& s) { return !I8 && s.own && (s.key_end & 15) != 0; }
+
 // All products, by one thread.
 template <int HD, bool I8>
 Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, I8>& sh) {
@@ -467,7 +474,7 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, 
   Ring<P::kStages> r(0);
   const uint32_t ring = smem_u32(smem) + P::kRing, q = smem_u32(smem) + P::kQ, pt = smem_u32(smem) + P::kP;
   const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kGroupRows;
-  uint32_t tile = 0, seg = 0;
+  uint32_t tile = 0, seg = 0, cleaned = 0;
   bool ok = true;
   Segment s{};
   while (ok && take(sh, p, seg, s)) {
@@ -501,22 +508,25 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, 
         const uint32_t g = tile + i - 1;
         if (i == 1 && seg > 0 && !(ok = wait(sh, p, &sh.o_free, (seg - 1) & 1))) break;
         if (!(ok = wait(sh, p, &sh.p_full, g & 1))) break;
+        if constexpr (!I8) {
+          if (i == s.tiles && needs_clean<I8>(s)) {  // all parts at once: the ring holds them
+            sh.clean_at = r.at;
+            Ring<P::kStages> ahead = r;
+            for (int c = 0; c < C && ok; ++c, ahead.step())
+              if ((ok = wait(sh, p, &sh.full[ahead.at], ahead.phase))) mbar_arrive(&sh.clean_ask[c]);
+            if (!ok) break;
+          }
+        }
         // the live keys, rounded up to 16
         const int live = min(kTileKeys, s.key_end - s.key0 - (i - 1) * kTileKeys);
         const int steps = (live + 15) >> 4;
         for (int c = 0; c < C; ++c) {
           if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
-          const int at = P::kRing + r.at * P::kStage;
-          if (!I8 && s.own && live < steps * 16) {
-            // what lies behind a sequence's own rows may be anything, and zero times a NaN
-            // is not zero
-            for (int x = live * 8; x < steps * 128; ++x)
-              for (int half = 0; half < 2; ++half)
-                *reinterpret_cast<uint4*>(smem + at + half * P::kSlab + x * 16) = make_uint4(0, 0, 0, 0);
-            fence_async_smem();
+          if constexpr (!I8) {
+            if (i == s.tiles && needs_clean<I8>(s) && !(ok = wait(sh, p, &sh.clean_done[c], cleaned & 1))) break;
           }
           tc_fence_after();
-          const uint32_t a = smem_u32(smem) + at, o_at = o_col + c * kGroupRows;
+          const uint32_t a = ring + r.at * P::kStage, o_at = o_col + c * kGroupRows;
           if (steps == kTileKeys / 16) {
 #pragma unroll
             for (int k = 0; k < 8; ++k)
@@ -526,12 +536,14 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, 
               tc_mma_f16(o_at, tc_desc(a + k * 2048, P::kSlab), tc_desc(pt + k * 2048, 0), id_o, i > 1 || k > 0);
           }
           tc_commit(&sh.empty[r.at]);
+          if (i == s.tiles) tc_commit(&sh.o_part[c]);  // 128 of the value dimensions are complete
           r.step();
         }
         if (!ok) break;
         tc_commit(&sh.pv_done);
       }
     }
+    if (needs_clean<I8>(s)) ++cleaned;
     tile += s.tiles;
     ++seg;
   }
@@ -593,7 +605,7 @@ Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, RingState<HD, t
 
 // One thread: a key of the tile (tensor-memory lane) and 32 of the 64 query rows.
 template <int HD, bool I8>
-Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh) {
+Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I8>& sh) {
   using P = Plan<HD, I8>;
   constexpr int C = HD / 128;
   const int tid = threadIdx.x - 128, lane = tid & 31, quarter = (tid >> 5) & 3, c0 = (tid >> 7) * 32;
@@ -604,6 +616,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh) {
   // once a wait has given up nothing waits any more, but every thread goes on to the end:
   // the barriers among these warps have no limit of their own
   bool ok = true;
+  uint32_t cleaned = 0;
   for (uint32_t seg = 0;; ++seg) {
     Segment s;
     if (softmax_any(!__all_sync(0xffffffffu, take(sh, p, seg, s)))) break;  // all warps or none
@@ -703,17 +716,33 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh) {
       if (lane == 0) mbar_arrive(&sh.p_full);
     }
 
-    // the segment's partial: thread = value dimension and, of up to 32 rows, half of the
-    // dimension blocks each; of more, half of the rows
-    ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);
-    tc_fence_after();
+    // the segment's partial, by blocks of 128 value dimensions as they are complete: thread =
+    // value dimension and, of up to 32 rows, half of the blocks each; of more, half of the rows
     float* const ml = (s.own ? p.own_ml : p.ml) + s.slot * (s.own ? p.own_rows : p.rows) * 2;
     float* const acc = (s.own ? p.own_acc : p.acc) + s.slot * (s.own ? p.own_rows : p.rows) * HD + key;
-    if (c0 < n) sh.wmax[quarter][c0 + lane] = lane_sums(l, lane);
+    if constexpr (!I8) {
+      if (needs_clean<I8>(s)) {
+        const int from = s.key_end & (kTileKeys - 1), chunks = (16 - (from & 15)) * 16;  // of both slabs
+        for (int c = 0; c < C; ++c) {
+          ok = ok && wait_warp(sh, p, &sh.clean_ask[c], cleaned & 1);
+          const int at = (sh.clean_at + c) % P::kStages;
+          if (tid < chunks)
+            *reinterpret_cast<uint4*>(smem + P::kRing + at * P::kStage + (tid & 1) * P::kSlab + from * 128 + (tid >> 1) * 16) =
+                make_uint4(0, 0, 0, 0);
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.clean_done[c]);
+        }
+        ++cleaned;
+      }
+    }
+    if (c0 < n) sh.wmax[quarter][c0 + lane] = lane_sums(l, lane);  // (while the last products run)
     const bool few = n <= 32;
     const int r0 = few ? 0 : c0, first = few && c0 > 0 ? C / 2 : 0, last = few && c0 == 0 ? C / 2 : C;
 #pragma unroll 1
     for (int c = first; c < last; ++c) {
+      ok = ok && wait_warp(sh, p, &sh.o_part[c], seg & 1);
+      tc_fence_after();
       float o[32];
       tmem_ld32(lanes + 2 * kGroupRows + c * kGroupRows + r0, o);
       tmem_wait_ld(o);
@@ -728,6 +757,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, State& sh) {
         if (r0 + i < s.n_rows) at[i * HD] = o[i];
     }
     softmax_sync();
+    // (P^T is free for the next segment: every warp has waited for a last block)
     if (tid < s.n_rows) {
       ml[2 * tid] = sh.ref[tid];
       ml[2 * tid + 1] = sh.wmax[0][tid] + sh.wmax[1][tid] + sh.wmax[2][tid] + sh.wmax[3][tid];
@@ -742,7 +772,7 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   RingState<HD, I8>& sh = *reinterpret_cast<RingState<HD, I8>*>(smem + P::kState);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Scheduler scheduler(p, lane);  // (warp 3's)
+  Scheduler scheduler(p);  // (warp 3's)
   if (warp == 1) {
     tmem_alloc(&sh.tmem, 512);
   } else if (warp == 2 && lane == 0) {
@@ -766,12 +796,19 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_free, 1);
+    for (int i = 0; i < 4; ++i) mbar_init(&sh.o_part[i], 1);
+    for (int i = 0; i < (I8 ? 0 : HD / 128); ++i) {
+      mbar_init(&sh.clean_ask[i], 1);
+      mbar_init(&sh.clean_done[i], kSoftmaxWarps);
+    }
     mbar_init(&sh.o_free, kSoftmaxWarps);
     mbar_init(&sh.drain, 1);
     sh.abort = 0;
     fence_mbar_init();
     fence_async_smem();
   }
+  pdl_wait();  // so far nothing of the kernel before was touched
+  if (warp == 3) scheduler.ask(p, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -866,6 +903,7 @@ __global__ void __launch_bounds__(32 * kJoinParts) shared_join_kernel(const Shar
   const float* const ml1 = p.own_ml + (s1 * p.own_rows + r1) * 2;
   float2 ml[kJoinMax / kJoinThreads];
   float R = -INFINITY;
+  pdl_launch_dependents();
   pdl_wait();  // all above comes from the call's own arguments
 #pragma unroll
   for (int k = 0; k < kEarly; ++k)
@@ -972,16 +1010,8 @@ constexpr int kMaxDevices = 64;
 
 template <int HD, int kJoinParts>
 cudaError_t launch_join(const SharedParams& p, cudaStream_t st) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(p.batch * p.n_q, HD / kJoinCols);
-  cfg.blockDim = dim3(32 * kJoinParts);
-  cfg.stream = st;
-  cudaLaunchAttribute at{};
-  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at.val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = &at;
-  cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, shared_join_kernel<HD, kJoinParts>, p);
+  return launch_pdl(shared_join_kernel<HD, kJoinParts>, dim3(p.batch * p.n_q, HD / kJoinCols), 32 * kJoinParts, 0, st, 1,
+                    p);
 }
 
 template <int HD, bool I8>
@@ -1001,8 +1031,8 @@ cudaError_t launch(const SharedMaps& maps, const SharedParams& p, cudaStream_t s
       configured[dev] = true;
     }
   }
-  shared_kernel<HD, I8><<<p.ctas, Plan<HD, I8>::kThreads, smem_bytes<HD, I8>(), st>>>(maps, p);
-  if ((e = cudaGetLastError()) != cudaSuccess) return e;
+  e = launch_pdl(shared_kernel<HD, I8>, dim3(p.ctas), Plan<HD, I8>::kThreads, smem_bytes<HD, I8>(), st, 1, maps, p);
+  if (e != cudaSuccess) return e;
   // warps for about five partials each
   const int n = (p.pieces > 0 ? p.pieces : p.prefix_tiles > 0 ? 2 : 0) + (p.own_cap + kTileKeys - 1) / kTileKeys;
   if (n <= 20) return launch_join<HD, 4>(p, st);

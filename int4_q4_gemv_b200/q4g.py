@@ -150,9 +150,16 @@ def check(status: int) -> None:
         raise Q4GError(status, f"{L.q4g_status_string(status).decode()}: {L.q4g_last_error().decode()}")
 
 
+_bound = {}  # name -> foreign function, looked up once
+
+
 def _call(name, *args):
-    st = getattr(lib(), name)(*args)
-    check(st)
+    fn = _bound.get(name)
+    if fn is None:
+        fn = _bound[name] = getattr(lib(), name)
+    st = fn(*args)
+    if st != Q4G_OK:
+        check(st)
 
 
 # ---- the C entry points, same names --------------------------------------
