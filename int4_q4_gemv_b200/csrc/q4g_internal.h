@@ -190,11 +190,11 @@ cudaError_t launch_step_init(const StepParams& p, cudaStream_t st);
 
 int device_sm_count();
 // Launch with programmatic stream serialization: the kernel may start while the one before
-// it in the stream ends, so it calls pdl_wait() before it touches global memory. With
-// cluster_x > 1 the grid's x extent is one cluster.
+// it in the stream ends, so it calls pdl_wait() before it touches global memory (pdl false:
+// after it). With cluster_x > 1 the grid's x extent is one cluster.
 template <typename... P, typename... A>
-cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, int cluster_x,
-                       A... args) {
+cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem, cudaStream_t st, bool pdl,
+                       int cluster_x, A... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = grid;
   cfg.blockDim = dim3(threads);
@@ -202,7 +202,7 @@ cudaError_t launch_pdl(void (*kernel)(P...), dim3 grid, int threads, size_t smem
   cfg.stream = st;
   cudaLaunchAttribute at[2]{};
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[0].val.programmaticStreamSerializationAllowed = pdl;
   at[1].id = cudaLaunchAttributeClusterDimension;
   at[1].val.clusterDim = {(unsigned)cluster_x, 1, 1};
   cfg.attrs = at;

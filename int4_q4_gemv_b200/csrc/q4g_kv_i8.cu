@@ -237,7 +237,7 @@ q4g_status launch(K kernel, int rows_at_once, const KvCopyParams& p, cudaStream_
   const int64_t need = ((int64_t)p.n * p.n_kv + rows_at_once - 1) / rows_at_once;
   const int64_t cap = 12ll * device_sm_count();  // for K and V each
   const dim3 grid((unsigned)(need < cap ? need : cap), 2);
-  const cudaError_t e = launch_pdl(kernel, grid, kKvThreads, 0, st, 1, p);
+  const cudaError_t e = launch_pdl(kernel, grid, kKvThreads, 0, st, true, 1, p);
   return e == cudaSuccess ? Q4G_OK : bad(Q4G_ECUDA, cudaGetErrorString(e));
 }
 

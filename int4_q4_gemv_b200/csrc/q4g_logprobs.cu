@@ -333,7 +333,7 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
   pdl_launch_dependents();
   if (TOP) {
     if (left < share_tiles || share == 0) sh.largest[share++][tid] = largest;
-    find_top(sh, x, rank * per, v_end, share, share_tiles * kVecs, skew, p.vocab, p.n_top);
+    find_top(sh, x, rank * per, v_end, share, min(share_tiles, tiles) * kVecs, skew, p.vocab, p.n_top);
   }
 
   // the CTA's statistics: lanes, then warps, in a fixed order
@@ -411,8 +411,11 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 template <int THREADS>
 cudaError_t launch_rows(const LogprobParams& p, int ranks, cudaStream_t st) {
   const dim3 grid(ranks, p.rows);
-  return p.n_top ? launch_pdl(logprob_kernel<true, THREADS>, grid, THREADS, 0, st, ranks, p)
-                 : launch_pdl(logprob_kernel<false, THREADS>, grid, THREADS, 0, st, ranks, p);
+  // many rows fill the GPU: CTAs that arrive while the kernel before ends gather on the SMs
+  // that it leaves first (256 rows of 262,144 logits: 44.6 us against 42.1)
+  constexpr bool pdl = THREADS == kLarge;
+  return p.n_top ? launch_pdl(logprob_kernel<true, THREADS>, grid, THREADS, 0, st, pdl, ranks, p)
+                 : launch_pdl(logprob_kernel<false, THREADS>, grid, THREADS, 0, st, pdl, ranks, p);
 }
 
 }  // namespace

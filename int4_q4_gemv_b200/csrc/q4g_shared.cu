@@ -50,6 +50,8 @@ constexpr int kMaxBatch = 256;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kSoftmaxWarps = 8;
 constexpr int kConvertWarps = 8;  // in two groups that take turns at the ring's items
+// Tensor memory columns: two S^T of 64, O^T, and for int8 rows two K parts of 128 x 128 fp16.
+constexpr int kKeyCol = 384, kKeyCols = 64;
 constexpr float kHeadroom = 8.f;  // a tile may pass the reference by 2^8
 constexpr float kOffset = 7.f;    // probabilities are scaled by 2^7: 2^15 at most
 constexpr float kLog2e = 1.4426950408889634f;
@@ -263,7 +265,7 @@ struct Plan {
   static constexpr int kState = kCodes + kCodeStages * kCodeStage;
 };
 
-constexpr int kQueue = 4;  // segments that the scheduling warp is ahead at most
+constexpr int kQueue = 2;  // segments that the scheduling warp is ahead at most
 
 // Barriers and small arrays of a CTA, apart from the ring's own barriers.
 struct State {
@@ -283,6 +285,7 @@ struct RingState : State {
   uint64_t full[Plan<HD, I8>::kStages], empty[Plan<HD, I8>::kStages];
   uint64_t clean_ask[I8 ? 1 : HD / 128], clean_done[I8 ? 1 : HD / 128];  // per V part of a segment's last tile
   uint64_t code_full[I8 ? Plan<HD, I8>::kCodeStages : 1], code_empty[I8 ? Plan<HD, I8>::kCodeStages : 1];
+  uint64_t k_full[I8 ? 2 : 1], k_empty[I8 ? 2 : 1];  // int8 K parts, widened into tensor memory
 };
 
 template <int HD, bool I8>
@@ -472,6 +475,7 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, 
   using P = Plan<HD, I8>;
   constexpr int C = HD / 128;
   Ring<P::kStages> r(0);
+  [[maybe_unused]] Ring<2> rk(0);
   const uint32_t ring = smem_u32(smem) + P::kRing, q = smem_u32(smem) + P::kQ, pt = smem_u32(smem) + P::kP;
   const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kGroupRows;
   uint32_t tile = 0, seg = 0, cleaned = 0;
@@ -490,15 +494,27 @@ Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, 
         const uint32_t g = tile + i, s_at = s_col + (g & 1) * kGroupRows;
         if (g >= 2 && !(ok = wait(sh, p, &sh.s_free[g & 1], (g / 2 - 1) & 1))) break;
         for (int c = 0; c < C; ++c) {
-          if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
-          tc_fence_after();
-          const uint32_t a = ring + r.at * P::kStage, b = q + 2 * c * P::kQSlab;
+          const uint32_t b = q + 2 * c * P::kQSlab;
+          if constexpr (I8) {
+            if (!(ok = wait(sh, p, &sh.k_full[rk.at], rk.phase))) break;
+            tc_fence_after();
+            const uint32_t a = sh.tmem + kKeyCol + rk.at * kKeyCols;
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            tc_mma_f16(s_at, tc_desc(a + (k >> 2) * P::kSlab + (k & 3) * 32, 0),
-                       tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
-          tc_commit(&sh.empty[r.at]);
-          r.step();
+            for (int k = 0; k < 8; ++k)
+              tc_mma_f16_ta(s_at, a + k * 8, tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
+            tc_commit(&sh.k_empty[rk.at]);
+            rk.step();
+          } else {
+            if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
+            tc_fence_after();
+            const uint32_t a = ring + r.at * P::kStage;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              tc_mma_f16(s_at, tc_desc(a + (k >> 2) * P::kSlab + (k & 3) * 32, 0),
+                         tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
+            tc_commit(&sh.empty[r.at]);
+            r.step();
+          }
         }
         if (!ok) break;
         tc_commit(&sh.s_full[g & 1]);
@@ -563,42 +579,81 @@ Q4G_DEV uint32_t widen2(uint32_t u, uint32_t sel) {
 
 constexpr int kGroup = kConvertWarps / 2 * 32;
 
+// 16 codes into 16 fp16 values.
+Q4G_DEV void widen16(uint4 u, uint32_t (&h)[8]) {
+  const uint32_t w[4] = {u.x ^ 0x80808080u, u.y ^ 0x80808080u, u.z ^ 0x80808080u, u.w ^ 0x80808080u};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) h[2 * k] = widen2(w[k], 0x4140), h[2 * k + 1] = widen2(w[k], 0x4342);
+}
+
+// Every second item of the code ring. K parts become operand A in tensor memory (a thread is
+// a key), V parts the swizzled slabs in shared memory that fp16 rows have: shared memory's
+// bandwidth bounds this path (a part of 16 KB of codes costs 16 to arrive, 16 to be read,
+// 32 to be written widened, 48 for its products), and a K part in tensor memory saves 64.
 template <int HD>
 Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh) {
   using P = Plan<HD, true>;
-  constexpr int NS = P::kStages, NC = P::kCodeStages, C = HD / 128;
-  const int tid = threadIdx.x - 32 * (4 + kSoftmaxWarps), lane = tid & 31, group = tid / kGroup;
-  uint32_t items = 0, seg = 0;
-  for (uint32_t it = group;; it += 2) {
-    while (it >= items) {
-      Segment s;
-      if (!__all_sync(0xffffffffu, take(sh, p, seg, s))) return;
-      if (lane == 0) give_back(sh, seg);
-      ++seg;
-      items += 2 * C * s.tiles;
-    }
-    const uint32_t cs = it % NC, st = it % NS;
-    if (!wait_warp(sh, p, &sh.code_full[cs], (it / NC) & 1)) return;
-    if (it >= NS && !wait_warp(sh, p, &sh.empty[st], (it / NS - 1) & 1)) return;
-    const unsigned char* const src = smem + P::kCodes + cs * P::kCodeStage;
-    unsigned char* const dst = smem + P::kRing + st * P::kStage;
+  constexpr int NC = P::kCodeStages, C = HD / 128;
+  const int tid = (threadIdx.x - 32 * (4 + kSoftmaxWarps)) % kGroup, lane = tid & 31;
+  const int group = (threadIdx.x - 32 * (4 + kSoftmaxWarps)) / kGroup;
+  const uint32_t key_lanes = sh.tmem + ((uint32_t)(tid & ~31) << 16) + kKeyCol;
+  Ring<NC> rc(0);
+  Ring<2> rk(1);
+  Ring<P::kStages> rv(1);
+  Segment s;
+  for (uint32_t seg = 0, it = 0; __all_sync(0xffffffffu, take(sh, p, seg, s)); ++seg) {
+    if (lane == 0) give_back(sh, seg);
+    for (int i = 0; i <= s.tiles; ++i) {
+      for (int part = 0; part < 2; ++part) {
+        if (i - part < 0 || i - part >= s.tiles) continue;
+        for (int c = 0; c < C; ++c, ++it) {
+          if ((int)(it & 1) == group) {
+            if (!wait_warp(sh, p, &sh.code_full[rc.at], rc.phase)) return;
+            const unsigned char* const src = smem + P::kCodes + rc.at * P::kCodeStage;
+            if (part == 0) {
+              if (!wait_warp(sh, p, &sh.k_empty[rk.at], rk.phase)) return;
+              tc_fence_after();
+#pragma unroll
+              for (int x = 0; x < 4; ++x) {
+                float v[16];
+#pragma unroll
+                for (int g = 0; g < 2; ++g) {
+                  uint32_t h[8];
+                  widen16(*reinterpret_cast<const uint4*>(src + tid * 128 + (((x * 2 + g) ^ (tid & 7)) * 16)), h);
+#pragma unroll
+                  for (int k = 0; k < 8; ++k) v[g * 8 + k] = __uint_as_float(h[k]);
+                }
+                tmem_st16(key_lanes + rk.at * kKeyCols + x * 16, v);
+              }
+              tmem_wait_st();
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.k_full[rk.at]);
+            } else {
+              if (!wait_warp(sh, p, &sh.empty[rv.at], rv.phase)) return;
+              unsigned char* const dst = smem + P::kRing + rv.at * P::kStage;
 #pragma unroll 4
-    for (int x = tid % kGroup; x < kTileKeys * 8; x += kGroup) {
-      const int row = x >> 3, g = x & 7;  // 16 codes: columns 16 g of the row
-      uint4 u = *reinterpret_cast<const uint4*>(src + x * 16);
-      u.x ^= 0x80808080u, u.y ^= 0x80808080u, u.z ^= 0x80808080u, u.w ^= 0x80808080u;
-      const uint4 a = make_uint4(widen2(u.x, 0x4140), widen2(u.x, 0x4342), widen2(u.y, 0x4140), widen2(u.y, 0x4342));
-      const uint4 b = make_uint4(widen2(u.z, 0x4140), widen2(u.z, 0x4342), widen2(u.w, 0x4140), widen2(u.w, 0x4342));
-      unsigned char* const out = dst + (g >> 2) * P::kSlab + row * 128;
-      const int c0 = 2 * (g & 3), first = g >> 2;  // the two slabs' lanes store different chunks at a time
-      *reinterpret_cast<uint4*>(out + (((c0 + first) ^ (row & 7)) * 16)) = first ? b : a;
-      *reinterpret_cast<uint4*>(out + (((c0 + 1 - first) ^ (row & 7)) * 16)) = first ? a : b;
-    }
-    fence_async_smem();
-    __syncwarp();
-    if (lane == 0) {
-      mbar_arrive(&sh.full[st]);
-      mbar_arrive(&sh.code_empty[cs]);
+              for (int x = tid; x < kTileKeys * 8; x += kGroup) {
+                const int row = x >> 3, g = x & 7;  // 16 codes: columns 16 g of the row
+                uint32_t h[8];
+                widen16(*reinterpret_cast<const uint4*>(src + row * 128 + ((g ^ (row & 7)) * 16)), h);
+                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
+                unsigned char* const out = dst + (g >> 2) * P::kSlab + row * 128;
+                const int c0 = 2 * (g & 3), first = g >> 2;  // the two slabs' lanes store different chunks at a time
+                *reinterpret_cast<uint4*>(out + (((c0 + first) ^ (row & 7)) * 16)) = first ? b : a;
+                *reinterpret_cast<uint4*>(out + (((c0 + 1 - first) ^ (row & 7)) * 16)) = first ? a : b;
+              }
+              fence_async_smem();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.full[rv.at]);
+            }
+            if (lane == 0) mbar_arrive(&sh.code_empty[rc.at]);
+          }
+          rc.step();
+          if (part == 0) rk.step();
+          else rv.step();
+        }
+      }
     }
   }
 }
@@ -779,6 +834,10 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     for (int i = 0; i < P::kStages; ++i) {
       mbar_init(&sh.full[i], I8 ? kConvertWarps / 2 : 1);
       mbar_init(&sh.empty[i], 1);
+    }
+    for (int i = 0; i < (I8 ? 2 : 0); ++i) {
+      mbar_init(&sh.k_full[i], kConvertWarps / 2);
+      mbar_init(&sh.k_empty[i], 1);
     }
     for (int i = 0; i < P::kCodeStages; ++i) {
       mbar_init(&sh.code_full[i], 1);
@@ -984,7 +1043,7 @@ EncodeTiled encode_tiled() {
   return fn;
 }
 
-// A tensor map over fp16 values (boxes of 64 columns, swizzled) or codes (128 columns).
+// A tensor map over fp16 values (boxes of 64 columns) or codes (128 columns), swizzled.
 // dims and box from the columns outwards, `rank` of them; stride[i]: elements between
 // neighbours of dimension i + 1. What a box has outside the tensor reads as zeros.
 bool encode(CUtensorMap* m, const void* base, bool i8, int rank, const int64_t* dims, const int64_t* stride,
@@ -995,8 +1054,7 @@ bool encode(CUtensorMap* m, const void* base, bool i8, int rank, const int64_t* 
   for (int i = 0; i + 1 < rank; ++i) s[i] = (cuuint64_t)stride[i] * (i8 ? 1 : 2);
   return encode_tiled()(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
                         const_cast<void*>(base), d, s, b, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                        i8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 // Rows [batch][rows][n_kv][hd]; a box is 128 keys of one KV head.
@@ -1010,8 +1068,8 @@ constexpr int kMaxDevices = 64;
 
 template <int HD, int kJoinParts>
 cudaError_t launch_join(const SharedParams& p, cudaStream_t st) {
-  return launch_pdl(shared_join_kernel<HD, kJoinParts>, dim3(p.batch * p.n_q, HD / kJoinCols), 32 * kJoinParts, 0, st, 1,
-                    p);
+  return launch_pdl(shared_join_kernel<HD, kJoinParts>, dim3(p.batch * p.n_q, HD / kJoinCols), 32 * kJoinParts, 0, st,
+                    true, 1, p);
 }
 
 template <int HD, bool I8>
@@ -1031,7 +1089,8 @@ cudaError_t launch(const SharedMaps& maps, const SharedParams& p, cudaStream_t s
       configured[dev] = true;
     }
   }
-  e = launch_pdl(shared_kernel<HD, I8>, dim3(p.ctas), Plan<HD, I8>::kThreads, smem_bytes<HD, I8>(), st, 1, maps, p);
+  e = launch_pdl(shared_kernel<HD, I8>, dim3(p.ctas), Plan<HD, I8>::kThreads, smem_bytes<HD, I8>(), st, true, 1, maps,
+                 p);
   if (e != cudaSuccess) return e;
   // warps for about five partials each
   const int n = (p.pieces > 0 ? p.pieces : p.prefix_tiles > 0 ? 2 : 0) + (p.own_cap + kTileKeys - 1) / kTileKeys;
