@@ -367,7 +367,15 @@ struct Scheduler {
   Q4G_DEV explicit Scheduler(const SharedParams& p) : work(p) { more = work.next(p, line, s); }
   Q4G_DEV void ask(const SharedParams& p, int lane) { len = lane < p.batch ? own_len_of(p, lane) : 0; }
   Q4G_DEV bool push(const SharedParams& p, State& sh, int lane) {
-    if (n >= kQueue && !wait_warp(sh, p, &sh.seg_empty[n % kQueue], (n / kQueue - 1) & 1)) return false;
+    // this wait lasts as long as a segment, which may be a whole prefix (the others: a tile)
+    bool room = n < kQueue;
+    for (int k = 0; k < 30 && !room && !sh.abort; ++k)
+      room = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.seg_empty[n % kQueue], (n / kQueue - 1) & 1, p.wait_ns));
+    if (!room) {
+      sh.abort = 1;
+      if (lane == 0) atomicOr(p.err, 1);
+      return false;
+    }
     if (lane == 0) {
       sh.seg[n % kQueue] = s;
       mbar_arrive(&sh.seg_full[n % kQueue]);  // releases the write above
@@ -873,9 +881,9 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   tc_fence_after();
   pdl_launch_dependents();  // the join's CTAs take the places that CTAs of this grid leave
   // With int8 rows 640 threads start with 96 registers each: the softmax warps take 128,
-  // (72 + 2 x 128 + 2 x 72) x 128 = 472 x 128 of 480 x 128.
+  // (80 + 2 x 128 + 2 x 72) x 128 = 480 x 128, all of them.
   if (warp < 4) {
-    if constexpr (I8) regs_dec<72>();
+    if constexpr (I8) regs_dec<80>();
     if (warp == 0) {
       if (elect_one()) produce<HD, I8>(p, maps, smem, sh);
       __syncwarp();

@@ -185,6 +185,46 @@ def test_all_values_zero(i8):
     assert torch.all(t.out == 0)
 
 
+@pytest.mark.parametrize("n_q,n_kv,hd", SHAPES)
+def test_no_rows_at_all(n_q, n_kv, hd):
+    for cap, lens in ((0, []), (40, [0, -1, 0])):
+        t = Batch(3, n_q, n_kv, hd, 0, cap, lens)
+        assert torch.all(t.run() == 0)
+
+
+def test_row_offsets_beyond_32_bits():
+    """A prefix whose K and V pass 4 GB each; the reference runs in pieces of keys."""
+    P, hd, batch = 4_300_077, 512, 2
+    t = Batch(batch, 16, 1, hd, 0, 8, [8, 3], seed=12)
+    t.prefix = P
+    t.kv[0] = torch.empty((P, 1, hd), dtype=torch.float16, device="cuda")
+    t.kv[1] = torch.empty((P, 1, hd), dtype=torch.float16, device="cuda")
+    g = gen(13)
+    step = 1 << 18
+    for x, w in zip(t.kv[:2], (hd ** -0.25, 1.0)):
+        for i in range(0, P, step):
+            x[i:i + step] = normal(g, x[i:i + step].shape, w)
+    t.kv[0][-5:] *= 3  # the last rows count
+    t.run()
+    q = t.q.double()
+    for b in range(batch):
+        n = int(t.len[b])
+        own = (t.rows(2, 0, b)[:n], t.rows(3, 0, b)[:n])
+        m = torch.full((16, 1), -1e300, dtype=torch.float64, device="cuda")
+        l, o, a, D, vmax = 0.0, 0.0, 0.0, 0.0, 0.0
+        for i in list(range(0, P, step)) + [None]:
+            k, v = own if i is None else (t.kv[0][i:i + step, 0].double(), t.kv[1][i:i + step, 0].double())
+            s = q[b] @ k.t()
+            new = torch.maximum(m, s.amax(-1, keepdim=True))
+            f, p = torch.exp(m - new), torch.exp(s - new)
+            l, o, a, m = l * f + p.sum(-1, keepdim=True), o * f + p @ v, a * f + p @ v.abs(), new
+            D = max(D, (hd / 16 + 18) * 2.0 ** -23 * float((q[b].abs() @ k.abs().t()).amax()))
+            vmax = max(vmax, float(v.abs().max()))
+        ref, a = o / l, a / l
+        tol = 2.0 ** -11 * ref.abs() + (2.0 ** -11 + 2 * D + 2.0 ** -20) * a + (P + n) * 2.0 ** -32 * vmax + 2.0 ** -25
+        assert bool(((t.out[b].double() - ref).abs() <= tol).all()), b
+
+
 def test_same_as_one_sequence_after_the_other():
     """Against the one-sequence entry point over prefix and own rows laid end to end."""
     t = Batch(3, 16, 1, 512, 1000, 50, [50, 1, 30], seed=8)
