@@ -240,6 +240,44 @@ def test_same_as_one_sequence_after_the_other():
         assert float((o.float() - t.out[b].float()).abs().max()) <= 4e-3
 
 
+@pytest.mark.parametrize("i8", [False, True])
+def test_a_nan_stays_with_its_sequence(i8):
+    """A NaN among one sequence's queries or own rows reaches that sequence alone."""
+    t = Batch(6, 16, 1, 512, 500, 40, [40, 7, 30, 0, 5, 40], i8, seed=14)
+    clean = t.run().clone()
+    t.q[1, 3, 100] = float("nan")
+    if i8:
+        t.kv[2][1][2, 4] = float("nan")
+        t.kv[3][1][5, 39] = float("nan")
+    else:
+        t.kv[2][2, 4, 0, 9] = float("nan")
+        t.kv[3][5, 39, 0, 11] = float("nan")
+    out = t.run()
+    assert torch.equal(out[[0, 3, 4]], clean[[0, 3, 4]])
+    assert torch.all(torch.isnan(out[1, 3])) and torch.equal(out[1, :3], clean[1, :3])
+    assert torch.equal(out[1, 4:], clean[1, 4:]) and torch.all(torch.isnan(out[2]))
+    if i8:
+        assert torch.all(torch.isnan(out[5]))
+    else:
+        assert torch.all(torch.isnan(out[5, :, 11])) and torch.equal(out[5, :, :11], clean[5, :, :11])
+
+
+def test_two_calls_at_once():
+    """Two streams, a workspace each, many calls in flight: the same bits as alone."""
+    a = Batch(9, 16, 1, 512, 4000, 200, [200, 1, 0, 33, 150, 128, 64, 90, 17], seed=15)
+    b = Batch(12, 16, 8, 256, 700, 60, list(range(0, 60, 5)), True, seed=16)
+    want = [t.run().clone() for t in (a, b)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    for _ in range(20):
+        for t, st in zip((a, b), streams):
+            with torch.cuda.stream(st):
+                t.out.zero_()
+                t.run()
+    torch.cuda.synchronize()
+    assert torch.equal(a.out, want[0]) and torch.equal(b.out, want[1])
+
+
 def test_repeats_bitwise_and_leaves_inputs_alone():
     t = Batch(6, 16, 1, 512, 3000, 64, [64, 0, 5, 32, 63, 1], seed=9)
     before = [x.clone() for x in t.kv] + [t.q.clone()]
