@@ -262,8 +262,8 @@ q4g_status q4g_flash_decode_shared_i8(const uint16_t* q, int32_t batch, int32_t 
  * inside [0, vocab). targets and logprob may both be NULL, so may entropy, and
  * top_ids and top_logprobs if n_top is 0 (either may be NULL otherwise, not both).
  * 0 <= rows <= 2^20, 1 <= vocab <= 2^30, 0 <= n_top <= min(32, vocab), temperature
- * finite and > 0. fp32 sums; the same bits on every call. Asynchronous, no scratch
- * memory, one launch. */
+ * finite, > 0 and not subnormal. fp32 sums; the same bits on every call.
+ * Asynchronous, no scratch memory, one launch. */
 #define Q4G_LOGPROBS_MAX_TOP 32
 q4g_status q4g_token_logprobs(const float* logits, int64_t rows, int64_t vocab, int64_t row_stride,
                               float temperature, const int32_t* targets, float* logprob, float* entropy,

@@ -6,18 +6,18 @@
 // Bound by HBM: 4 bytes per logit, read once. Every thread keeps its own running
 // (m, S, E = sum exp(d) d) and rescales them when its maximum moves; E counts from
 // the maximum, so the entropy is a sum of terms of one sign and cancels nothing.
-// The alternatives cost the pass nothing: it leaves the largest logit of every share (a
-// thread's logits in an eighth of the CTA's tiles), and the n_top best logits of a CTA's
-// part lie in the shares whose largest is at least the n_top-th largest of those (n_top
-// logits reach it). Only these n_top of some 2000 shares are read again. (Shares of whole
-// threads read 42 MB again for 256 rows with 20 alternatives, 60 us against 50; lists kept
-// up to date while reading, per
-// CTA or per warp, took 98 and 106 us on 256 rows of 262,144 logits with 20 alternatives,
-// 52 and 60 more than without alternatives.)
-// A row is split over the CTAs of one thread-block cluster when there are few rows;
-// they join through distributed shared memory, in rank order, without scratch memory
-// or atomics between CTAs: the sums do not depend on timing, nor does the answer on
-// the order in which candidates enter the buffer (it is sorted by value and index).
+// The alternatives cost the pass little: it leaves the largest logit of every share (a
+// thread's logits in an eighth of a CTA's tiles), and the n_top best logits of a CTA's part
+// lie in the shares whose largest is at least the n_top-th largest of those (n_top logits
+// reach it). Only these n_top of some 2000 shares are read again, and what reaches that
+// value is sorted. On 256 rows of 262,144 logits (268 MB, 41.0 us at the measured copy
+// rate) 42 to 44 us without alternatives, 50 to 52 us with 20; tried instead: shares of
+// whole threads (42 MB read again) 60 us, lists kept up to date while reading 98 (a CTA's)
+// and 106 us (a warp's), bulk copies into a ring in shared memory 55 without alternatives.
+// A row is split over the CTAs of one thread-block cluster when there are few rows; they
+// join through distributed shared memory, in rank order, without scratch memory or atomics
+// between CTAs. The sums depend on no timing; candidates arrive in any order, and sorting
+// them by value and index gives the same list each time.
 #include <math.h>
 
 #include "../../include/q4g.h"
@@ -166,10 +166,10 @@ Q4G_DEV void take_in(Top& t, u64* wait, int lane, int n_top) {
 Q4G_DEV float4 load_piece(const float* x, int v, int v_end, int skew, int vocab) {
   const int first = 4 * v - skew;
   if (v < v_end && first >= 0 && first + 3 < vocab) {
-    const uint4 u = ld_stream_u4(x + first);
+    const uint4 u = ld_stream_u4_ordered(x + first);
     return make_float4(__uint_as_float(u.x), __uint_as_float(u.y), __uint_as_float(u.z), __uint_as_float(u.w));
   }
-  auto one = [&](int i) { return v < v_end && i >= 0 && i < vocab ? __ldg(x + i) : -INFINITY; };
+  auto one = [&](int i) { return v < v_end && i >= 0 && i < vocab ? x[i] : -INFINITY; };
   return make_float4(one(first), one(first + 1), one(first + 2), one(first + 3));
 }
 
@@ -191,12 +191,11 @@ Q4G_DEV void read_again(const LpShared<THREADS>& sh, const float* x, int v_begin
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, n_hits = sh.n_hits;
   for (int h = warp; h < n_hits; h += THREADS / 32) {
     const int share = sh.hits[h] / THREADS, v_hit = v_begin + share * per * THREADS + sh.hits[h] % THREADS;
-    const int pieces = per;
-    for (int q0 = 0; q0 < pieces; q0 += 64) {
+    for (int q0 = 0; q0 < per; q0 += 64) {
       float4 f[2];
 #pragma unroll
       for (int b = 0; b < 2; ++b)
-        f[b] = load_piece(x, q0 + 32 * b + lane < pieces ? v_hit + (q0 + 32 * b + lane) * THREADS : v_end, v_end, skew,
+        f[b] = load_piece(x, q0 + 32 * b + lane < per ? v_hit + (q0 + 32 * b + lane) * THREADS : v_end, v_end, skew,
                           vocab);
 #pragma unroll
       for (int b = 0; b < 2; ++b) {
@@ -206,7 +205,7 @@ Q4G_DEV void read_again(const LpShared<THREADS>& sh, const float* x, int v_begin
         for (int j = 0; j < 4; ++j) {
           if (__any_sync(0xffffffffu, e[j] >= thr)) {
             const int i = 4 * v - skew + j;
-            take(make_key(e[j], i), e[j] >= thr && q0 + 32 * b + lane < pieces && v < v_end && i >= 0 && i < vocab);
+            take(make_key(e[j], i), e[j] >= thr && q0 + 32 * b + lane < per && v < v_end && i >= 0 && i < vocab);
           }
         }
       }
@@ -424,8 +423,8 @@ cudaError_t q4g::launch_logprobs(const LogprobParams& p, cudaStream_t st) {
   // Few rows: clusters of CTAs of 1024 threads, an SM each, so that a row's loads are all
   // in flight within a few tiles (three quarters of the SMs: more clusters do not fit on the
   // GPU at once, 16 rows as 16 clusters of 8 took 22 us, as clusters of 4 they take 12). Many:
-  // CTAs of 256 threads, four on every SM at most, the number that fits:
-  // one wave, 42 us for 256 rows of 262,144 logits against 47 with up to six.
+  // CTAs of 256 threads, four on every SM at most, the number that fits: one wave, 42 us for
+  // 256 rows of 262,144 logits against 47 with up to six.
   const int sms = device_sm_count();
   const bool large = (int64_t)p.rows * kMaxCluster <= sms && p.vocab > 2 * tile_of(kSmall);
   const int64_t tiles = ((int64_t)p.vocab + tile_of(large ? kLarge : kSmall) - 1) / tile_of(large ? kLarge : kSmall);

@@ -696,8 +696,8 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
       const bool live = left > 0;
       float ks = kLog2e, vs = 1.f, lift = 0.f;  // lift: log2 of the V scale, for the reference only
       if constexpr (I8) {
-        ks = live ? __ldg(ks_at) * kLog2e : 0.f;
-        vs = live ? __ldg(vs_at) : 0.f;
+        ks = live ? *ks_at * kLog2e : 0.f;
+        vs = live ? *vs_at : 0.f;
         lift = __log2f(fmaxf(fabsf(vs), 9.094947e-13f));  // 2^-40 at least
         ks_at += kTileKeys * p.n_kv;
         vs_at += kTileKeys * p.n_kv;
@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   Scheduler scheduler(p);  // (warp 3's)
   if (warp == 1) {
-    tmem_alloc(&sh.tmem, 512);
+    tmem_alloc(&sh.tmem, 512);  // at once: with 227 KB of shared memory the CTA is alone on its SM
   } else if (warp == 2 && lane == 0) {
     for (int i = 0; i < P::kStages; ++i) {
       mbar_init(&sh.full[i], I8 ? kConvertWarps / 2 : 1);
@@ -1223,7 +1223,8 @@ q4g_status run_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_k
 
 extern "C" size_t q4g_flash_decode_shared_workspace_bytes(int32_t batch, int32_t n_q, int32_t n_kv,
                                                           int32_t head_dim) {
-  if (batch < 1 || n_q < 1 || n_kv < 1 || head_dim < 1 || n_q < n_kv) return 256;
+  // (a call with such sizes is refused)
+  if (batch < 1 || batch > kMaxBatch || n_kv < 1 || n_q < n_kv || n_q > 1024 || head_dim < 1 || head_dim > 512) return 256;
   SharedParams p{};
   p.batch = batch, p.n_q = n_q, p.n_kv = n_kv;
   return plan_scratch(p, head_dim, nullptr);
