@@ -49,7 +49,7 @@ constexpr int kGroupRows = 64;   // query rows of one unit, at most
 constexpr int kMaxBatch = 256;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kSoftmaxWarps = 8;
-constexpr int kConvertWarps = 8;  // in two groups that take turns at the ring's items
+constexpr int kConvertWarps = 12;  // int8 rows: a group of four for K parts, two that take turns for V parts
 // Tensor memory columns: two S^T of 64, O^T, and for int8 rows two K parts of 128 x 128 fp16.
 constexpr int kKeyCol = 384, kKeyCols = 64;
 constexpr float kHeadroom = 8.f;  // a tile may pass the reference by 2^8
@@ -150,7 +150,7 @@ Q4G_DEV int line_piece(const Line& w, int64_t t) {
 }
 
 struct Segment {
-  int own, b, h, g0, n_rows;  // first sequence and head, query rows
+  int16_t own, b, h, g0, n_rows;  // first sequence and head, query rows
   int key0, key_end, tiles;   // keys [key0, key_end) of the unit's rows
   int64_t slot;
 };
@@ -244,25 +244,31 @@ struct Work {
 };
 
 // ------------------------------------------------------------- shared memory ----
-// A ring stage holds 128 keys x 128 columns of K or V in fp16, as two swizzled slabs of 64
-// columns (V's two are the M = 128 of one product). int8 rows arrive in a second ring of
-// 16 KB stages and are widened into it. (Single slabs as K's items gave the ring another
-// half stage and let it go earlier, but each item costs the products 50 ns: 3.5 us a tile
-// of 64 rows against 3.0.)
+// A ring stage holds two boxes of 64 keys x 64 columns in fp16, swizzled: a K part is 64
+// columns of a tile's 128 keys (the boxes one below the other are one operand of 128 rows),
+// a V part 64 keys of 128 value dimensions (the boxes are the two halves of M = 128). With
+// parts of twice the size, 128 keys x 128 columns, less of the ring was on its way at a time.
+// int8 rows arrive in a second ring, 128 keys x 128 codes a stage, and are widened.
 template <int HD, bool I8>
 struct Plan {
-  static constexpr int kStages = I8 ? 3 : (HD == 512 ? 4 : 5);
-  static constexpr int kCodeStages = I8 ? (HD == 512 ? 3 : 5) : 0;
+  static constexpr int kStages = I8 || HD == 512 ? 4 : 5;
+  static constexpr int kHalves = I8 ? 2 : 1;  // V parts of 128 value dimensions
+  // codes: stages of K parts and of V parts (those and V's ring stages even: each of the two
+  // groups that widen V has its own)
+  static constexpr int kKeyCodes = I8 ? (HD == 512 ? 2 : 4) : 0, kValueCodes = I8 ? 4 : 0;
+  static constexpr int kProbs = I8 ? 2 : 1;  // buffers of P^T
   static constexpr int kThreads = 32 * (4 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
-  static constexpr int kSlab = kTileKeys * 128;  // bytes
-  static constexpr int kStage = 2 * kSlab;
-  static constexpr int kCodeStage = kTileKeys * 128;
+  static constexpr int kStage = kTileKeys * 256 / kHalves;  // bytes
+  static constexpr int kBox = kStage / 2;                   // a block of 64 columns
+  static constexpr int kKeyCode = kTileKeys * 128, kValueCode = kKeyCode / kHalves;
   static constexpr int kQSlab = kGroupRows * 128;
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + HD / 64 * kQSlab;
-  static constexpr int kRing = kP + kTileKeys * 128;
+  static constexpr int kPBytes = kTileKeys * 128;
+  static constexpr int kRing = kP + kProbs * kPBytes;
   static constexpr int kCodes = kRing + kStages * kStage;
-  static constexpr int kState = kCodes + kCodeStages * kCodeStage;
+  static constexpr int kValues = kCodes + kKeyCodes * kKeyCode;
+  static constexpr int kState = kValues + kValueCodes * kValueCode;
 };
 
 constexpr int kQueue = 2;  // segments that the scheduling warp is ahead at most
@@ -274,18 +280,30 @@ struct State {
   float factor[kGroupRows];
   Segment seg[kQueue];
   uint64_t seg_full[kQueue], seg_empty[kQueue];
-  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_free, o_part[4], o_free, drain;
+  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free, drain[2];
   int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
   int32_t clean_at;  // the ring stage of the first V part to clear
   volatile int abort;
 };
+// fp16 rows: the last tile's V parts to clear; int8 rows: the ring of codes, and that of
+// their K parts, widened into tensor memory.
 template <int HD, bool I8>
-struct RingState : State {
-  uint64_t full[Plan<HD, I8>::kStages], empty[Plan<HD, I8>::kStages];
-  uint64_t clean_ask[I8 ? 1 : HD / 128], clean_done[I8 ? 1 : HD / 128];  // per V part of a segment's last tile
-  uint64_t code_full[I8 ? Plan<HD, I8>::kCodeStages : 1], code_empty[I8 ? Plan<HD, I8>::kCodeStages : 1];
-  uint64_t k_full[I8 ? 2 : 1], k_empty[I8 ? 2 : 1];  // int8 K parts, widened into tensor memory
+struct RowState {
+  uint64_t clean_ask[HD / 128], clean_done[HD / 128];
+};
+template <int HD>
+struct RowState<HD, true> {
+  // codes of K and of V parts, and K parts widened into tensor memory
+  static constexpr int NK = Plan<HD, true>::kKeyCodes, NV = Plan<HD, true>::kValueCodes;
+  uint64_t kc_full[NK], kc_empty[NK], vc_full[NV], vc_empty[NV], k_full[2], k_empty[2];
+};
+template <int HD, bool I8>
+struct RingState : State, RowState<HD, I8> {
+  // a ring stage's fills with K and with V parts ([1]; all fills with int8 rows) have a
+  // barrier each: one consumer then waits for all of a barrier's phases, in order
+  uint64_t full[2][Plan<HD, I8>::kStages], empty[Plan<HD, I8>::kStages];
+  uint64_t o_part[HD / 128];  // 128 value dimensions of a segment's O^T are complete
 };
 
 template <int HD, bool I8>
@@ -417,56 +435,97 @@ struct Ring {
     if (++at == N) at = 0, phase ^= 1;
   }
 };
+// A ring in which K and V parts alternate as the producer lays them out, for one consumer of
+// one kind: a phase bit per stage, as that kind's fills of a stage are counted.
+template <int N>
+struct PartRing {
+  int at = 0;
+  uint32_t bits = 0;
+  Q4G_DEV uint32_t phase() const { return (bits >> at) & 1; }
+  Q4G_DEV void step() {
+    bits ^= 1u << at;
+    if (++at == N) at = 0;
+  }
+  Q4G_DEV void skip(int n) {  // the other kind's parts, n <= N
+    at += n;
+    if (at >= N) at -= N;
+  }
+};
 
-// All copies, by one thread: a segment's queries, then ring items in the order in which the
-// products take them: in step i the K parts of tile i, then the V parts of tile i - 1.
+// All copies of keys and values, by one thread: in step i the K parts of tile i and the V
+// parts of tile i - 1, whose products run beside each other. fp16 rows: one ring, all of K
+// before V; int8 rows: a ring of codes for each, in turn. An issue takes about 0.1 us, so a
+// part is one copy, and the queries are left to the thread that multiplies with them.
 // (Asking L2 for the next tile as well, by prefetch copies, was slower at every length.)
 template <int HD, bool I8>
 Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned char* smem, RingState<HD, I8>& sh) {
   using P = Plan<HD, I8>;
-  constexpr int N = I8 ? P::kCodeStages : P::kStages;
-  Ring<N> r(1);  // the phase before a stage's first use: that wait is over at once
-  uint64_t* const full = I8 ? sh.code_full : sh.full;
-  uint64_t* const empty = I8 ? sh.code_empty : sh.empty;
+  constexpr int C = HD / 128, NK = I8 ? P::kKeyCodes : P::kStages, NV = I8 ? P::kValueCodes : 1;
+  Ring<NK> rk(1);  // the phase before a stage's first use: that wait is over at once
+  [[maybe_unused]] Ring<NV> rv(1);
   uint32_t seg = 0, items = 0;
+  uint32_t fills = 0, last = 0;  // a bit per stage: K fills (and from bit 16 on V fills) so far odd; the last was V
   bool ok = true;
   Segment s{};
   while (ok && take(sh, p, seg, s)) {
     give_back(sh, seg);
-    if (seg > 0 && !(ok = wait(sh, p, &sh.q_free, (seg - 1) & 1))) break;
     ++seg;
-    mbar_arrive_expect_tx(&sh.q_full, HD * 2 * p.heads * (s.own ? 1 : p.seqs));
-#pragma unroll 1
-    for (int c = 0; c < HD / 64; ++c)
-      tma_load_4d(smem + P::kQ + c * P::kQSlab, s.own ? &maps.own_q : &maps.q, c * 64, s.g0, s.h, s.b, &sh.q_full);
+    const void* const k_map = s.own ? &maps.own_k : &maps.k;
+    const void* const v_map = s.own ? &maps.own_v : &maps.v;
+    const int b = s.own ? s.b : 0, h = s.h;
     for (int i = 0; i <= s.tiles && ok; ++i) {
-      for (int part = 0; part < 2 && ok; ++part) {
-        const int j = i - part;
-        if (j < 0 || j >= s.tiles) continue;
-        const void* const map = s.own ? (part ? &maps.own_v : &maps.own_k) : (part ? &maps.v : &maps.k);
-        const int key = s.key0 + j * kTileKeys;
-        for (int c = 0; c < HD / 128; ++c) {
-          if (!(ok = wait(sh, p, &empty[r.at], r.phase))) break;
-          unsigned char* dst = smem + (I8 ? P::kCodes + r.at * P::kCodeStage : P::kRing + r.at * P::kStage);
-          mbar_arrive_expect_tx(&full[r.at], I8 ? P::kCodeStage : P::kStage);
-#pragma unroll
-          for (int half = 0; half < (I8 ? 1 : 2); ++half, dst += P::kSlab) {
-            const int x = c * 128 + half * 64;
-            if (s.own) tma_load_4d(dst, map, x, s.h, key, s.b, &full[r.at]);
-            else tma_load_3d(dst, map, x, s.h, key, &full[r.at]);
+      const int key = s.key0 + i * kTileKeys;
+      if constexpr (I8) {
+#pragma unroll 1
+        for (int c = 0; c < C; ++c) {
+          if (i < s.tiles) {
+            if (!(ok = wait(sh, p, &sh.kc_empty[rk.at], rk.phase))) break;
+            mbar_arrive_expect_tx(&sh.kc_full[rk.at], P::kKeyCode);
+            tma_load_5d(smem + P::kCodes + rk.at * P::kKeyCode, k_map, 0, key, c, h, b, &sh.kc_full[rk.at]);
+            fills ^= 1u << rk.at;
+            rk.step();
           }
-          r.step();
-          ++items;
+          for (int half = 0; half < P::kHalves && i > 0; ++half) {
+            if (!(ok = wait(sh, p, &sh.vc_empty[rv.at], rv.phase))) break;
+            mbar_arrive_expect_tx(&sh.vc_full[rv.at], P::kValueCode);
+            tma_load_5d(smem + P::kValues + rv.at * P::kValueCode, v_map, 0, key - kTileKeys + half * 64, c, h, b,
+                        &sh.vc_full[rv.at]);
+            fills ^= 1u << (16 + rv.at);
+            rv.step();
+          }
+          if (!ok) break;
+        }
+      } else {
+        for (int part = 0; part < 2 && ok; ++part) {
+          if (part == 0 ? i == s.tiles : i == 0) continue;
+          const void* const map = part ? v_map : k_map;
+#pragma unroll 1
+          for (int c = 0; c < C; ++c) {
+            if (!(ok = wait(sh, p, &sh.empty[rk.at], rk.phase))) break;
+            uint64_t* const bar = (part ? sh.full[1] : sh.full[0]) + rk.at;
+            mbar_arrive_expect_tx(bar, P::kStage);
+            tma_load_5d(smem + P::kRing + rk.at * P::kStage, map, 0, part ? key - kTileKeys : key, 2 * c, h, b, bar);
+            fills ^= 1u << (16 * part + rk.at);
+            last = (last & ~(1u << rk.at)) | ((uint32_t)part << rk.at);
+            ++items;
+            rk.step();
+          }
         }
       }
     }
   }
-  // Given up: the copies in flight still write this CTA's shared memory. Each is the last
-  // of its stage, so its phase stays.
+  // Given up: the copies in flight still write this CTA's shared memory. Each is the last of
+  // its stage (and, of a stage with one barrier for K and one for V, kind), so its phase stays.
   if (!ok || sh.abort) {
-    for (uint32_t k = items > N ? items - N : 0; k < items; ++k)
-      mbar_wait_bounded(&full[k % N], (k / N) & 1, 20000000ull);
-    if (seg > 0) mbar_wait_bounded(&sh.q_full, (seg - 1) & 1, 20000000ull);
+    if constexpr (I8) {  // a stage that was never filled has no phase to wait for: that wait is over at once
+      for (int k = 0; k < NK; ++k) mbar_wait_bounded(&sh.kc_full[k], ((fills >> k) & 1) ^ 1, 20000000ull);
+      for (int k = 0; k < NV; ++k) mbar_wait_bounded(&sh.vc_full[k], ((fills >> (16 + k)) & 1) ^ 1, 20000000ull);
+    } else {
+      for (int k = 0; k < NK && k < (int)items; ++k) {
+        const int kind = (last >> k) & 1;
+        mbar_wait_bounded((kind ? sh.full[1] : sh.full[0]) + k, ((fills >> (16 * kind + k)) & 1) ^ 1, 20000000ull);
+      }
+    }
   }
 }
 
@@ -477,103 +536,144 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
 template <bool I8>
 Q4G_DEV bool needs_clean(const Segment& s) { return !I8 && s.own && (s.key_end & 15) != 0; }
 
-// All products, by one thread.
+// The products, by two threads of two warps: the issuing thread, not the tensor core, is what
+// a product waits for (one thread with descriptors made for each product and a wait every 8
+// took 73 cycles a product; with one addition per descriptor 61; two threads 48, n = 64).
+//
+// S^T of a segment's tiles; the segment's queries.
 template <int HD, bool I8>
-Q4G_DEV void multiply(const SharedParams& p, unsigned char* smem, RingState<HD, I8>& sh) {
+Q4G_DEV void multiply_keys(const SharedParams& p, const SharedMaps& maps, unsigned char* smem, RingState<HD, I8>& sh) {
   using P = Plan<HD, I8>;
   constexpr int C = HD / 128;
-  Ring<P::kStages> r(0);
+  [[maybe_unused]] PartRing<P::kStages> r;
   [[maybe_unused]] Ring<2> rk(0);
-  const uint32_t ring = smem_u32(smem) + P::kRing, q = smem_u32(smem) + P::kQ, pt = smem_u32(smem) + P::kP;
-  const uint32_t s_col = sh.tmem, o_col = sh.tmem + 2 * kGroupRows;
+  const uint64_t ring = tc_desc(smem_u32(smem) + P::kRing, 0), q = tc_desc(smem_u32(smem) + P::kQ, 0);
+  const uint32_t s_col = sh.tmem;
+  uint32_t tile = 0, seg = 0;
+  bool ok = true;
+  Segment s{};
+  while (ok && take(sh, p, seg, s)) {
+    give_back(sh, seg);
+    const uint32_t id = tc_idesc_f16((s.n_rows + 15) & ~15, false, false);
+    if (seg > 0 && !(ok = wait(sh, p, &sh.q_free, (seg - 1) & 1))) break;
+    mbar_arrive_expect_tx(&sh.q_full, HD * 2 * p.heads * (s.own ? 1 : p.seqs));
+#pragma unroll 1
+    for (int c = 0; c < HD / 64; ++c)
+      tma_load_4d(smem + P::kQ + c * P::kQSlab, s.own ? &maps.own_q : &maps.q, c * 64, s.g0, s.h, s.b, &sh.q_full);
+    if (!(ok = wait(sh, p, &sh.q_full, seg & 1))) {
+      mbar_wait_bounded(&sh.q_full, seg & 1, 20000000ull);  // the copies write this CTA's shared memory
+      break;
+    }
+    for (int i = 0; i < s.tiles && ok; ++i, ++tile) {
+      const uint32_t s_at = s_col + (tile & 1) * kGroupRows;
+      if (tile >= 2 && !(ok = wait(sh, p, &sh.s_free[tile & 1], (tile / 2 - 1) & 1))) break;
+#pragma unroll 1
+      for (int c = 0; c < C; ++c) {
+        if constexpr (I8) {
+          if (!(ok = wait(sh, p, &sh.k_full[rk.at], rk.phase))) break;
+          tc_fence_after();
+          const uint32_t a = sh.tmem + kKeyCol + rk.at * kKeyCols;
+          const uint64_t b = q + c * (2 * P::kQSlab >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_f16_ta(s_at, a + k * 8, b + (k >> 2) * (P::kQSlab >> 4) + (k & 3) * 2, id, c > 0 || k > 0);
+          tc_commit(&sh.k_empty[rk.at]);
+          rk.step();
+        } else {
+          if (!(ok = wait(sh, p, &sh.full[0][r.at], r.phase()))) break;
+          tc_fence_after();
+          const uint64_t a = ring + r.at * (P::kStage >> 4), b = q + c * (2 * P::kQSlab >> 4);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            tc_mma_f16(s_at, a + (k >> 2) * (P::kBox >> 4) + (k & 3) * 2, b + (k >> 2) * (P::kQSlab >> 4) + (k & 3) * 2,
+                       id, c > 0 || k > 0);
+          tc_commit(&sh.empty[r.at]);
+          r.step();
+        }
+      }
+      if (!ok) break;
+      tc_commit(&sh.s_full[tile & 1]);
+      if (i == s.tiles - 1) tc_commit(&sh.q_free);
+      if constexpr (!I8) {  // the parts of V that follow: the tile's before, and the last one's
+        if (i > 0) r.skip(C);
+        if (i == s.tiles - 1) r.skip(C);
+      }
+    }
+    ++seg;
+  }
+  if (!ok || sh.abort) {  // given up: products in flight still use shared and tensor memory
+    tc_commit(&sh.drain[0]);
+    mbar_wait_bounded(&sh.drain[0], 0, p.wait_ns);
+  }
+}
+
+// O^T += V^T P^T.
+template <int HD, bool I8>
+Q4G_DEV void multiply_values(const SharedParams& p, unsigned char* smem, RingState<HD, I8>& sh) {
+  using P = Plan<HD, I8>;
+  constexpr int C = HD / 128;
+  PartRing<P::kStages> r;
+  const uint64_t ring = tc_desc(smem_u32(smem) + P::kRing, P::kBox), pt = tc_desc(smem_u32(smem) + P::kP, 0);
+  const uint32_t o_col = sh.tmem + 2 * kGroupRows;
   uint32_t tile = 0, seg = 0, cleaned = 0;
   bool ok = true;
   Segment s{};
   while (ok && take(sh, p, seg, s)) {
     give_back(sh, seg);
-    const uint32_t n = (s.n_rows + 15) & ~15;
-    const uint32_t id_s = tc_idesc_f16(n, false, false), id_o = tc_idesc_f16(n, true, true);
-    if (!(ok = wait(sh, p, &sh.q_full, seg & 1))) break;
-    // Step i: S^T of tile i, then O^T += V^T P^T of tile i - 1, whose softmax ran while S^T
-    // of tile i was made. (Part by part in turn, with a tile more between the two, was 7%
-    // slower on 16 sequences and a 32K prefix: every part then pays the wait for its load.)
-    for (int i = 0; i <= s.tiles && ok; ++i) {
-      if (i < s.tiles) {
-        const uint32_t g = tile + i, s_at = s_col + (g & 1) * kGroupRows;
-        if (g >= 2 && !(ok = wait(sh, p, &sh.s_free[g & 1], (g / 2 - 1) & 1))) break;
-        for (int c = 0; c < C; ++c) {
-          const uint32_t b = q + 2 * c * P::kQSlab;
-          if constexpr (I8) {
-            if (!(ok = wait(sh, p, &sh.k_full[rk.at], rk.phase))) break;
-            tc_fence_after();
-            const uint32_t a = sh.tmem + kKeyCol + rk.at * kKeyCols;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16_ta(s_at, a + k * 8, tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
-            tc_commit(&sh.k_empty[rk.at]);
-            rk.step();
-          } else {
-            if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
-            tc_fence_after();
-            const uint32_t a = ring + r.at * P::kStage;
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16(s_at, tc_desc(a + (k >> 2) * P::kSlab + (k & 3) * 32, 0),
-                         tc_desc(b + (k >> 2) * P::kQSlab + (k & 3) * 32, 0), id_s, c > 0 || k > 0);
-            tc_commit(&sh.empty[r.at]);
-            r.step();
-          }
+    const uint32_t id = tc_idesc_f16((s.n_rows + 15) & ~15, true, true);
+    const bool clean = needs_clean<I8>(s);
+    if (!I8) r.skip(C);  // the first tile's K parts
+    if (seg > 0 && !(ok = wait(sh, p, &sh.o_free, (seg - 1) & 1))) break;
+    for (int i = 0; i < s.tiles && ok; ++i, ++tile) {
+      const bool last = i == s.tiles - 1;
+      if (!I8 && !last) r.skip(C);  // the next tile's K parts
+      const int buf = tile % P::kProbs;
+      if (!(ok = wait(sh, p, &sh.p_full[buf], (tile / P::kProbs) & 1))) break;
+      // the live keys, rounded up to 16
+      const int live = min(kTileKeys, s.key_end - s.key0 - i * kTileKeys);
+      const int steps = (live + 15) >> 4;
+      if constexpr (!I8) {
+        if (last && clean) {  // all parts at once: the ring holds them
+          PartRing<P::kStages> ahead = r;
+          sh.clean_at = ahead.at;
+          for (int c = 0; c < C && ok; ++c, ahead.step())
+            if ((ok = wait(sh, p, &sh.full[1][ahead.at], ahead.phase()))) mbar_arrive(&sh.clean_ask[c]);
+          if (!ok) break;
         }
-        if (!ok) break;
-        tc_commit(&sh.s_full[g & 1]);
-        if (i == s.tiles - 1) tc_commit(&sh.q_free);
       }
-      if (i > 0) {
-        const uint32_t g = tile + i - 1;
-        if (i == 1 && seg > 0 && !(ok = wait(sh, p, &sh.o_free, (seg - 1) & 1))) break;
-        if (!(ok = wait(sh, p, &sh.p_full, g & 1))) break;
+      const uint64_t pb = pt + buf * (P::kPBytes >> 4);
+#pragma unroll 1
+      for (int c = 0; c < P::kHalves * C; ++c) {
+        if (!(ok = wait(sh, p, &sh.full[1][r.at], r.phase()))) break;
+        constexpr int kSteps = 8 / P::kHalves;
+        const int d = c / P::kHalves, half = c % P::kHalves;
         if constexpr (!I8) {
-          if (i == s.tiles && needs_clean<I8>(s)) {  // all parts at once: the ring holds them
-            sh.clean_at = r.at;
-            Ring<P::kStages> ahead = r;
-            for (int c = 0; c < C && ok; ++c, ahead.step())
-              if ((ok = wait(sh, p, &sh.full[ahead.at], ahead.phase))) mbar_arrive(&sh.clean_ask[c]);
-            if (!ok) break;
-          }
+          if (last && clean && !(ok = wait(sh, p, &sh.clean_done[d], cleaned & 1))) break;
         }
-        // the live keys, rounded up to 16
-        const int live = min(kTileKeys, s.key_end - s.key0 - (i - 1) * kTileKeys);
-        const int steps = (live + 15) >> 4;
-        for (int c = 0; c < C; ++c) {
-          if (!(ok = wait(sh, p, &sh.full[r.at], r.phase))) break;
-          if constexpr (!I8) {
-            if (i == s.tiles && needs_clean<I8>(s) && !(ok = wait(sh, p, &sh.clean_done[c], cleaned & 1))) break;
-          }
-          tc_fence_after();
-          const uint32_t a = ring + r.at * P::kStage, o_at = o_col + c * kGroupRows;
-          if (steps == kTileKeys / 16) {
+        tc_fence_after();
+        const uint64_t a = ring + r.at * (P::kStage >> 4), b = pb + half * (kSteps * 128);
+        const uint32_t o_at = o_col + d * kGroupRows;
+        if (steps == kTileKeys / 16) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-              tc_mma_f16(o_at, tc_desc(a + k * 2048, P::kSlab), tc_desc(pt + k * 2048, 0), id_o, i > 1 || k > 0);
-          } else {
-            for (int k = 0; k < steps; ++k)
-              tc_mma_f16(o_at, tc_desc(a + k * 2048, P::kSlab), tc_desc(pt + k * 2048, 0), id_o, i > 1 || k > 0);
-          }
-          tc_commit(&sh.empty[r.at]);
-          if (i == s.tiles) tc_commit(&sh.o_part[c]);  // 128 of the value dimensions are complete
-          r.step();
+          for (int k = 0; k < kSteps; ++k) tc_mma_f16(o_at, a + k * 128, b + k * 128, id, i > 0 || half > 0 || k > 0);
+        } else {
+#pragma unroll 1
+          for (int k = 0; k < kSteps && half * kSteps + k < steps; ++k)
+            tc_mma_f16(o_at, a + k * 128, b + k * 128, id, i > 0 || half > 0 || k > 0);
         }
-        if (!ok) break;
-        tc_commit(&sh.pv_done);
+        tc_commit(&sh.empty[r.at]);
+        if (last && half == P::kHalves - 1) tc_commit(&sh.o_part[d]);  // 128 of the value dimensions are complete
+        r.step();
       }
+      if (!ok) break;
+      tc_commit(&sh.pv_done[buf]);
     }
-    if (needs_clean<I8>(s)) ++cleaned;
-    tile += s.tiles;
+    if (clean) ++cleaned;
     ++seg;
   }
-  if (!ok || sh.abort) {  // given up: products in flight still use shared and tensor memory
-    tc_commit(&sh.drain);
-    mbar_wait_bounded(&sh.drain, 0, p.wait_ns);
+  if (!ok || sh.abort) {  // as above
+    tc_commit(&sh.drain[1]);
+    mbar_wait_bounded(&sh.drain[1], 0, p.wait_ns);
   }
 }
 
@@ -585,7 +685,7 @@ Q4G_DEV uint32_t widen2(uint32_t u, uint32_t sel) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-constexpr int kGroup = kConvertWarps / 2 * 32;
+constexpr int kGroup = 128;  // threads that widen a part
 
 // 16 codes into 16 fp16 values.
 Q4G_DEV void widen16(uint4 u, uint32_t (&h)[8]) {
@@ -594,74 +694,95 @@ Q4G_DEV void widen16(uint4 u, uint32_t (&h)[8]) {
   for (int k = 0; k < 4; ++k) h[2 * k] = widen2(w[k], 0x4140), h[2 * k + 1] = widen2(w[k], 0x4342);
 }
 
-// Every second item of the code ring. K parts become operand A in tensor memory (a thread is
-// a key), V parts the swizzled slabs in shared memory that fp16 rows have: shared memory's
-// bandwidth bounds this path (a part of 16 KB of codes costs 16 to arrive, 16 to be read,
-// 32 to be written widened, 48 for its products), and a K part in tensor memory saves 64.
+// K parts become operand A in tensor memory (a thread is a key).
 template <int HD>
-Q4G_DEV void convert(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh) {
+Q4G_DEV void convert_keys(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh) {
   using P = Plan<HD, true>;
-  constexpr int NC = P::kCodeStages, C = HD / 128;
-  const int tid = (threadIdx.x - 32 * (4 + kSoftmaxWarps)) % kGroup, lane = tid & 31;
-  const int group = (threadIdx.x - 32 * (4 + kSoftmaxWarps)) / kGroup;
+  const int tid = threadIdx.x & (kGroup - 1), lane = tid & 31;
   const uint32_t key_lanes = sh.tmem + ((uint32_t)(tid & ~31) << 16) + kKeyCol;
-  Ring<NC> rc(0);
+  Ring<P::kKeyCodes> rc(0);
   Ring<2> rk(1);
-  Ring<P::kStages> rv(1);
   Segment s;
-  for (uint32_t seg = 0, it = 0; __all_sync(0xffffffffu, take(sh, p, seg, s)); ++seg) {
+  for (uint32_t seg = 0; __all_sync(0xffffffffu, take(sh, p, seg, s)); ++seg) {
     if (lane == 0) give_back(sh, seg);
-    for (int i = 0; i <= s.tiles; ++i) {
-      for (int part = 0; part < 2; ++part) {
-        if (i - part < 0 || i - part >= s.tiles) continue;
-        for (int c = 0; c < C; ++c, ++it) {
-          if ((int)(it & 1) == group) {
-            if (!wait_warp(sh, p, &sh.code_full[rc.at], rc.phase)) return;
-            const unsigned char* const src = smem + P::kCodes + rc.at * P::kCodeStage;
-            if (part == 0) {
-              if (!wait_warp(sh, p, &sh.k_empty[rk.at], rk.phase)) return;
-              tc_fence_after();
+#pragma unroll 1
+    for (int c = 0; c < s.tiles * (HD / 128); ++c) {
+      if (!wait_warp(sh, p, &sh.kc_full[rc.at], rc.phase)) return;
+      const unsigned char* const src = smem + P::kCodes + rc.at * P::kKeyCode + tid * 128;
+      if (!wait_warp(sh, p, &sh.k_empty[rk.at], rk.phase)) return;
+      tc_fence_after();
 #pragma unroll
-              for (int x = 0; x < 4; ++x) {
-                float v[16];
+      for (int half = 0; half < 2; ++half) {
+        uint4 u[4];
 #pragma unroll
-                for (int g = 0; g < 2; ++g) {
-                  uint32_t h[8];
-                  widen16(*reinterpret_cast<const uint4*>(src + tid * 128 + (((x * 2 + g) ^ (tid & 7)) * 16)), h);
+        for (int x = 0; x < 4; ++x) u[x] = *reinterpret_cast<const uint4*>(src + (((half * 4 + x) ^ (tid & 7)) * 16));
+        if (half == 1) {  // the codes are in registers: their stage is free
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.kc_empty[rc.at]);
+        }
 #pragma unroll
-                  for (int k = 0; k < 8; ++k) v[g * 8 + k] = __uint_as_float(h[k]);
-                }
-                tmem_st16(key_lanes + rk.at * kKeyCols + x * 16, v);
-              }
-              tmem_wait_st();
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.k_full[rk.at]);
-            } else {
-              if (!wait_warp(sh, p, &sh.empty[rv.at], rv.phase)) return;
-              unsigned char* const dst = smem + P::kRing + rv.at * P::kStage;
-#pragma unroll 4
-              for (int x = tid; x < kTileKeys * 8; x += kGroup) {
-                const int row = x >> 3, g = x & 7;  // 16 codes: columns 16 g of the row
-                uint32_t h[8];
-                widen16(*reinterpret_cast<const uint4*>(src + row * 128 + ((g ^ (row & 7)) * 16)), h);
-                const uint4 a = make_uint4(h[0], h[1], h[2], h[3]), b = make_uint4(h[4], h[5], h[6], h[7]);
-                unsigned char* const out = dst + (g >> 2) * P::kSlab + row * 128;
-                const int c0 = 2 * (g & 3), first = g >> 2;  // the two slabs' lanes store different chunks at a time
-                *reinterpret_cast<uint4*>(out + (((c0 + first) ^ (row & 7)) * 16)) = first ? b : a;
-                *reinterpret_cast<uint4*>(out + (((c0 + 1 - first) ^ (row & 7)) * 16)) = first ? a : b;
-              }
-              fence_async_smem();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(&sh.full[rv.at]);
-            }
-            if (lane == 0) mbar_arrive(&sh.code_empty[rc.at]);
+        for (int x = 0; x < 2; ++x) {
+          float v[16];
+#pragma unroll
+          for (int g = 0; g < 2; ++g) {
+            uint32_t h[8];
+            widen16(u[2 * x + g], h);
+#pragma unroll
+            for (int k = 0; k < 8; ++k) v[g * 8 + k] = __uint_as_float(h[k]);
           }
-          rc.step();
-          if (part == 0) rk.step();
-          else rv.step();
+          tmem_st16(key_lanes + rk.at * kKeyCols + half * 32 + x * 16, v);
         }
       }
+      rc.step();
+      tmem_wait_st();
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.k_full[rk.at]);
+      rk.step();
+    }
+  }
+}
+
+// V parts become the swizzled blocks in shared memory that fp16 rows have, by halves of 64
+// keys; two groups take turns at the halves. A thread has 16 of the 128 columns in every
+// 16th key. Eight lanes have the first half of a key's columns and the second half of its
+// neighbour's: reads and both writes of 16 bytes then fall on different banks.
+template <int HD>
+Q4G_DEV void convert_values(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh, int group) {
+  using P = Plan<HD, true>;
+  const int tid = threadIdx.x & (kGroup - 1), lane = tid & 31;
+  const int g = tid & 7, row = (tid >> 3) ^ (g >> 2), c0 = 2 * (g & 3);
+  const int from = row * 128 + ((g ^ (row & 7)) * 16);
+  const int to = (g >> 2) * P::kBox + row * 128, to0 = to + ((c0 ^ (row & 7)) * 16), to1 = to0 ^ 16;
+  Ring<P::kValueCodes> rc(0);
+  Ring<P::kStages> rv(1);
+  Segment s;
+  if (group == 1) rc.step(), rv.step();
+  for (uint32_t seg = 0; __all_sync(0xffffffffu, take(sh, p, seg, s)); ++seg) {
+    if (lane == 0) give_back(sh, seg);
+#pragma unroll 1
+    for (int c = 0; c < s.tiles * (HD / 128); ++c) {
+      if (!wait_warp(sh, p, &sh.vc_full[rc.at], rc.phase)) return;
+      const unsigned char* const src = smem + P::kValues + rc.at * P::kValueCode + from;
+      uint4 u[4];
+#pragma unroll
+      for (int x = 0; x < 4; ++x) u[x] = *reinterpret_cast<const uint4*>(src + x * 2048);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.vc_empty[rc.at]);
+      if (!wait_warp(sh, p, &sh.empty[rv.at], rv.phase)) return;
+      unsigned char* const dst = smem + P::kRing + rv.at * P::kStage;
+#pragma unroll
+      for (int x = 0; x < 4; ++x) {
+        uint32_t h[8];
+        widen16(u[x], h);
+        *reinterpret_cast<uint4*>(dst + to0 + x * 2048) = make_uint4(h[0], h[1], h[2], h[3]);
+        *reinterpret_cast<uint4*>(dst + to1 + x * 2048) = make_uint4(h[4], h[5], h[6], h[7]);
+      }
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.full[1][rv.at]);
+      rc.step(), rc.step();
+      rv.step(), rv.step();
     }
   }
 }
@@ -738,7 +859,11 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
         if (j == 0 || raise) sh.ref[tid] = m;
       }
       raise = softmax_any(raise);
-      if (j > 0) ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);  // P^T and O^T are free
+      // P^T's buffer is free; and O^T if it changes here
+      constexpr uint32_t NB = P::kProbs;
+      const uint32_t pb = tile % NB;
+      if (tile >= NB) ok = ok && wait_warp(sh, p, &sh.pv_done[pb], (tile / NB - 1) & 1);
+      if (NB > 1 && raise) ok = ok && wait_warp(sh, p, &sh.pv_done[(tile - 1) % NB], ((tile - 1) / NB) & 1);
       if (active) {
         if (raise) {
           tc_fence_after();
@@ -758,7 +883,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
 #pragma unroll
           for (int i = 0; i < 32; ++i) l[i] *= sh.factor[c0 + i];
         }
-        unsigned char* const row = smem + P::kP + key * 128;
+        unsigned char* const row = smem + P::kP + pb * P::kPBytes + key * 128;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
           uint32_t h[4];
@@ -776,7 +901,7 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full);
+      if (lane == 0) mbar_arrive(&sh.p_full[pb]);
     }
 
     // the segment's partial, by blocks of 128 value dimensions as they are complete: thread =
@@ -785,12 +910,12 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
     float* const acc = (s.own ? p.own_acc : p.acc) + s.slot * (s.own ? p.own_rows : p.rows) * HD + key;
     if constexpr (!I8) {
       if (needs_clean<I8>(s)) {
-        const int from = s.key_end & (kTileKeys - 1), chunks = (16 - (from & 15)) * 16;  // of both slabs
+        const int from = s.key_end & (kTileKeys - 1), chunks = (16 - (from & 15)) * 16;  // of both boxes
         for (int c = 0; c < C; ++c) {
           ok = ok && wait_warp(sh, p, &sh.clean_ask[c], cleaned & 1);
           const int at = (sh.clean_at + c) % P::kStages;
           if (tid < chunks)
-            *reinterpret_cast<uint4*>(smem + P::kRing + at * P::kStage + (tid & 1) * P::kSlab + from * 128 + (tid >> 1) * 16) =
+            *reinterpret_cast<uint4*>(smem + P::kRing + at * P::kStage + (tid & 1) * P::kBox + from * 128 + (tid >> 1) * 16) =
                 make_uint4(0, 0, 0, 0);
           fence_async_smem();
           __syncwarp();
@@ -840,36 +965,45 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     tmem_alloc(&sh.tmem, 512);  // at once: with 227 KB of shared memory the CTA is alone on its SM
   } else if (warp == 2 && lane == 0) {
     for (int i = 0; i < P::kStages; ++i) {
-      mbar_init(&sh.full[i], I8 ? kConvertWarps / 2 : 1);
+      mbar_init(&sh.full[0][i], 1);
+      mbar_init(&sh.full[1][i], I8 ? kGroup / 32 : 1);
       mbar_init(&sh.empty[i], 1);
     }
-    for (int i = 0; i < (I8 ? 2 : 0); ++i) {
-      mbar_init(&sh.k_full[i], kConvertWarps / 2);
-      mbar_init(&sh.k_empty[i], 1);
-    }
-    for (int i = 0; i < P::kCodeStages; ++i) {
-      mbar_init(&sh.code_full[i], 1);
-      mbar_init(&sh.code_empty[i], kConvertWarps / 2);
+    if constexpr (I8) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&sh.k_full[i], kGroup / 32);
+        mbar_init(&sh.k_empty[i], 1);
+      }
+      for (int i = 0; i < P::kKeyCodes; ++i) {
+        mbar_init(&sh.kc_full[i], 1);
+        mbar_init(&sh.kc_empty[i], kGroup / 32);
+      }
+      for (int i = 0; i < P::kValueCodes; ++i) {
+        mbar_init(&sh.vc_full[i], 1);
+        mbar_init(&sh.vc_empty[i], kGroup / 32);
+      }
+    } else {
+      for (int i = 0; i < HD / 128; ++i) {
+        mbar_init(&sh.clean_ask[i], 1);
+        mbar_init(&sh.clean_done[i], kSoftmaxWarps);
+      }
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 2 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
+      mbar_init(&sh.seg_empty[i], 3 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kSoftmaxWarps);
+      mbar_init(&sh.p_full[i], kSoftmaxWarps);
+      mbar_init(&sh.pv_done[i], 1);
     }
-    mbar_init(&sh.p_full, kSoftmaxWarps);
-    mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_free, 1);
-    for (int i = 0; i < 4; ++i) mbar_init(&sh.o_part[i], 1);
-    for (int i = 0; i < (I8 ? 0 : HD / 128); ++i) {
-      mbar_init(&sh.clean_ask[i], 1);
-      mbar_init(&sh.clean_done[i], kSoftmaxWarps);
-    }
+    for (int i = 0; i < HD / 128; ++i) mbar_init(&sh.o_part[i], 1);
     mbar_init(&sh.o_free, kSoftmaxWarps);
-    mbar_init(&sh.drain, 1);
+    mbar_init(&sh.drain[0], 1);
+    mbar_init(&sh.drain[1], 1);
     sh.abort = 0;
     fence_mbar_init();
     fence_async_smem();
@@ -880,26 +1014,30 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   __syncthreads();
   tc_fence_after();
   pdl_launch_dependents();  // the join's CTAs take the places that CTAs of this grid leave
-  // With int8 rows 640 threads start with 96 registers each: the softmax warps take 128,
-  // (80 + 2 x 128 + 2 x 72) x 128 = 480 x 128, all of them.
+  // With int8 rows 768 threads start with 80 registers each: the softmax warps take 120,
+  // (64 + 2 x 120 + 3 x 56) x 128 = 472 x 128 of 480 x 128.
   if (warp < 4) {
-    if constexpr (I8) regs_dec<80>();
+    if constexpr (I8) regs_dec<64>();
     if (warp == 0) {
       if (elect_one()) produce<HD, I8>(p, maps, smem, sh);
       __syncwarp();
     } else if (warp == 1) {
-      if (elect_one()) multiply<HD, I8>(p, smem, sh);
+      if (elect_one()) multiply_keys<HD, I8>(p, maps, smem, sh);
+      __syncwarp();
+    } else if (warp == 2) {
+      if (elect_one()) multiply_values<HD, I8>(p, smem, sh);
       __syncwarp();
     } else if (warp == 3) {
       scheduler.run(p, sh, lane);
     }
   } else if (warp < 4 + kSoftmaxWarps) {
-    if constexpr (I8) regs_inc<128>();
+    if constexpr (I8) regs_inc<120>();
     softmax<HD, I8>(p, smem, sh);
   } else {
     if constexpr (I8) {
-      regs_dec<72>();
-      convert<HD>(p, smem, sh);
+      regs_dec<56>();
+      if (warp < 8 + kSoftmaxWarps) convert_keys<HD>(p, smem, sh);
+      else convert_values<HD>(p, smem, sh, (warp >> 2) & 1);
     }
   }
   tc_fence_before();
@@ -1056,8 +1194,8 @@ EncodeTiled encode_tiled() {
 // neighbours of dimension i + 1. What a box has outside the tensor reads as zeros.
 bool encode(CUtensorMap* m, const void* base, bool i8, int rank, const int64_t* dims, const int64_t* stride,
             const int32_t* box) {
-  cuuint64_t d[4], s[3];
-  cuuint32_t b[4], one[4] = {1, 1, 1, 1};
+  cuuint64_t d[5], s[4];
+  cuuint32_t b[5], one[5] = {1, 1, 1, 1, 1};
   for (int i = 0; i < rank; ++i) d[i] = (cuuint64_t)dims[i], b[i] = (cuuint32_t)box[i];
   for (int i = 0; i + 1 < rank; ++i) s[i] = (cuuint64_t)stride[i] * (i8 ? 1 : 2);
   return encode_tiled()(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
@@ -1065,11 +1203,14 @@ bool encode(CUtensorMap* m, const void* base, bool i8, int rank, const int64_t* 
                         CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Rows [batch][rows][n_kv][hd]; a box is 128 keys of one KV head.
-bool encode_rows(CUtensorMap* m, const void* base, bool i8, int rank, int hd, int n_kv, int64_t rows, int batch) {
-  const int64_t dims[] = {hd, n_kv, rows, batch}, stride[] = {hd, (int64_t)n_kv * hd, rows * n_kv * hd};
-  const int32_t box[] = {i8 ? 128 : 64, 1, kTileKeys, 1};
-  return encode(m, base, i8, rank, dims, stride, box);
+// Rows [batch][rows][n_kv][hd], the columns as blocks of 128 bytes: a box is `keys` keys
+// of 128 columns, one block behind the other.
+bool encode_rows(CUtensorMap* m, const void* base, bool i8, int hd, int n_kv, int64_t rows, int batch, int keys) {
+  const int cols = i8 ? 128 : 64;
+  const int64_t row = (int64_t)n_kv * hd, dims[] = {cols, rows, hd / cols, n_kv, batch},
+                stride[] = {row, cols, hd, rows * row};
+  const int32_t box[] = {cols, keys, 128 / cols, 1, 1};
+  return encode(m, base, i8, 5, dims, stride, box);
 }
 
 constexpr int kMaxDevices = 64;
@@ -1207,11 +1348,13 @@ q4g_status run_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_k
   const int32_t q_box[] = {64, p.heads, 1, p.seqs}, own_q_box[] = {64, p.heads, 1, 1};
   bool ok = encode(&maps.q, q, false, 4, q_dims, q_stride, q_box) &&
             encode(&maps.own_q, q, false, 4, q_dims, q_stride, own_q_box);
+  const int v_keys = i8 ? kTileKeys / 2 : kTileKeys;
   if (prefix > 0)
-    ok = ok && encode_rows(&maps.k, kp, i8, 3, hd, n_kv, prefix, 1) && encode_rows(&maps.v, vp, i8, 3, hd, n_kv, prefix, 1);
+    ok = ok && encode_rows(&maps.k, kp, i8, hd, n_kv, prefix, 1, kTileKeys) &&
+         encode_rows(&maps.v, vp, i8, hd, n_kv, prefix, 1, v_keys);
   if (own_cap > 0)
-    ok = ok && encode_rows(&maps.own_k, ko, i8, 4, hd, n_kv, own_cap, batch) &&
-         encode_rows(&maps.own_v, vo, i8, 4, hd, n_kv, own_cap, batch);
+    ok = ok && encode_rows(&maps.own_k, ko, i8, hd, n_kv, own_cap, batch, kTileKeys) &&
+         encode_rows(&maps.own_v, vo, i8, hd, n_kv, own_cap, batch, v_keys);
   if (!ok) return bad(Q4G_ECUDA, "tensor map refused by the driver");
   cudaError_t e;
   if (hd == 512) e = i8 ? launch<512, true>(maps, p, st) : launch<512, false>(maps, p, st);
