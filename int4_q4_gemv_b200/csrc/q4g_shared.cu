@@ -68,6 +68,8 @@ struct SharedParams {
   int32_t rows, own_rows;       // query rows that a partial of either kind holds
   int32_t ctas;
   int32_t prefix_tiles, pieces, prefix_ctas;  // pieces of a prefix unit; 0: the units as one line
+  int32_t piece_tiles, longer;                // the first `longer` pieces of a unit have one tile more
+  uint32_t piece_inv, group_inv;              // reciprocals of pieces and groups (small_quotient)
   // partials: (reference, sum) per row, then O per row; the prefix units' slots, then the own units'
   float *ml, *acc, *own_ml, *own_acc;
   __half* out;
@@ -98,6 +100,9 @@ Q4G_DEV int64_t quotient(int64_t a, int64_t b) {
   }
   return ((a | b) >> 32) == 0 ? (int64_t)((uint32_t)a / (uint32_t)b) : a / b;
 }
+// a / b for a, b < 2^16, from inv = ceil(2^32 / b): the excess of a * inv is below 2^32 / b. A
+// CTA starts with two of these.
+Q4G_DEV int small_quotient(int a, uint32_t inv, int b) { return b == 1 ? a : (int)__umulhi((uint32_t)a, inv); }
 Q4G_DEV int64_t cut_begin(int64_t total, int ctas, int c) { return ctas > 0 ? quotient(total * c, ctas) : 0; }
 Q4G_DEV int cut_of(int64_t total, int ctas, int64_t t) { return (int)quotient((t + 1) * ctas - 1, total); }
 
@@ -137,7 +142,7 @@ Q4G_DEV Line make_line(const SharedParams& p, const int32_t* own_places) {
   w.own_places = own_places;
   w.total = (int64_t)own_places[p.batch] * p.n_kv * p.parts;
   const int idle = p.ctas - p.prefix_ctas;
-  const int64_t load = p.pieces > 0 ? (p.prefix_tiles + p.pieces - 1) / p.pieces + kUnitCost : 0;
+  const int64_t load = p.pieces > 0 ? p.piece_tiles + (p.longer > 0) + kUnitCost : 0;
   if (idle == 0) w.head = 0;
   else if (w.total <= idle * load || p.prefix_ctas == 0) w.head = w.total;
   else w.head = quotient(idle * (p.prefix_ctas * load + w.total), p.ctas);
@@ -192,19 +197,20 @@ struct Work {
       if (!own) {
         int u;
         if (p.pieces > 0) {
-          u = (int)quotient(t, p.pieces);
+          u = small_quotient((int)t, p.piece_inv, p.pieces);
           const int k = (int)t - u * p.pieces;
-          first = (int)quotient((int64_t)p.prefix_tiles * k, p.pieces);
-          s.tiles = (int)quotient((int64_t)p.prefix_tiles * (k + 1), p.pieces) - first;
+          first = k * p.piece_tiles + min(k, p.longer);
+          s.tiles = p.piece_tiles + (k < p.longer);
           s.slot = t;
           t = end;
+          s.h = small_quotient(u, p.group_inv, p.groups);
         } else {
           const int n = places_h(p);
           u = (int)quotient(t, n);
           s.slot = (int64_t)u + blockIdx.x;
           advance(t - (int64_t)u * n, n, first, s.tiles);
+          s.h = (int)quotient(u, p.groups);
         }
-        s.h = (int)quotient(u, p.groups);
         const int grp = u - s.h * p.groups;
         s.b = p.parts == 1 ? grp * p.seqs : grp / p.parts;
         s.g0 = p.parts == 1 ? 0 : grp % p.parts * kGroupRows;
@@ -377,13 +383,15 @@ struct Scheduler {
   Work work;
   Line line{};
   Segment s{};
-  bool more;
-  int len;
   uint32_t n = 0;
-  // before the CTA's first barrier: the first prefix segment comes from the arguments alone,
-  // then (memory may be read) the first own lengths are asked for
-  Q4G_DEV explicit Scheduler(const SharedParams& p) : work(p) { more = work.next(p, line, s); }
-  Q4G_DEV void ask(const SharedParams& p, int lane) { len = lane < p.batch ? own_len_of(p, lane) : 0; }
+  // The first prefix segment comes from the arguments alone and is queued by the thread that
+  // makes the barriers, so that nobody sleeps for it.
+  Q4G_DEV explicit Scheduler(const SharedParams& p) : work(p) {}
+  Q4G_DEV void push_first(const SharedParams& p, State& sh) {
+    if (!work.next(p, line, s)) return;
+    sh.seg[0] = s;
+    mbar_arrive(&sh.seg_full[0]);
+  }
   Q4G_DEV bool push(const SharedParams& p, State& sh, int lane) {
     // this wait lasts as long as a segment, which may be a whole prefix (the others: a tile)
     bool room = n < kQueue;
@@ -401,16 +409,20 @@ struct Scheduler {
     ++n;
     return true;
   }
-  Q4G_DEV void run(const SharedParams& p, State& sh, int lane) {
-    for (int kind = 0; kind < 2; ++kind) {
-      for (; more; more = work.next(p, line, s))
-        if (!push(p, sh, lane)) return;
-      if (kind == 0) {
+  Q4G_DEV void run(const SharedParams& p, State& sh, int lane, int len) {
+    bool first = true;
+    for (;;) {
+      if (work.next(p, line, s)) {
+        if (first && !work.own) n = 1;  // push_first() has queued it
+        else if (!push(p, sh, lane)) return;
+        first = false;
+      } else if (!work.own) {
         sum_own_places(p, sh.own_places, lane, len);
         __syncwarp();
         line = make_line(p, sh.own_places);
         work.start_own(p, line);
-        more = work.next(p, line, s);
+      } else {
+        break;
       }
     }
     s.tiles = 0;
@@ -960,7 +972,7 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   extern __shared__ __align__(1024) unsigned char smem[];
   RingState<HD, I8>& sh = *reinterpret_cast<RingState<HD, I8>*>(smem + P::kState);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  Scheduler scheduler(p);  // (warp 3's)
+  int len = 0;  // of own rows: warp 3's
   if (warp == 1) {
     tmem_alloc(&sh.tmem, 512);  // at once: with 227 KB of shared memory the CTA is alone on its SM
   } else if (warp == 2 && lane == 0) {
@@ -1006,10 +1018,11 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     mbar_init(&sh.drain[1], 1);
     sh.abort = 0;
     fence_mbar_init();
+    Scheduler(p).push_first(p, sh);
     fence_async_smem();
   }
   pdl_wait();  // so far nothing of the kernel before was touched
-  if (warp == 3) scheduler.ask(p, lane);
+  if (warp == 3 && lane < p.batch) len = own_len_of(p, lane);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -1028,7 +1041,7 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
       if (elect_one()) multiply_values<HD, I8>(p, smem, sh);
       __syncwarp();
     } else if (warp == 3) {
-      scheduler.run(p, sh, lane);
+      Scheduler(p).run(p, sh, lane, len);
     }
   } else if (warp < 4 + kSoftmaxWarps) {
     if constexpr (I8) regs_inc<120>();
@@ -1273,6 +1286,10 @@ void plan_prefix(SharedParams& p, int64_t prefix, int64_t own_cap) {
     if (best == 0 || cost < best) best = cost, p.pieces = (int32_t)pieces;
   }
   p.prefix_ctas = (int32_t)(p.pieces * units);
+  p.piece_tiles = p.prefix_tiles / p.pieces;
+  p.longer = p.prefix_tiles % p.pieces;
+  p.piece_inv = (uint32_t)((((uint64_t)1 << 32) + p.pieces - 1) / p.pieces);
+  p.group_inv = (uint32_t)((((uint64_t)1 << 32) + p.groups - 1) / p.groups);
 }
 
 // Units, partial slots and the scratch layout; returns its bytes.
