@@ -26,10 +26,13 @@
 // 128-key tiles over the CTAs, those without a prefix piece first. Every piece leaves one
 // partial (reference, sum, O), and a second kernel joins each row's partials.
 //
-// Bound by HBM for one row group (a 128-key tile of hd 512 is 256 KB, 5.6 us of an SM's
-// share of HBM; its products take 64 x 68 cycles, 2.2 us: a product with M = 128 reads
-// 4 KB of A from shared memory in 64 cycles, whatever n up to 64); by the products above
-// two row groups.
+// Bound by HBM for one row group: a 128-key tile of hd 512 is 256 KB, 5.6 us of an SM's
+// share of HBM (4 sequences of 16 heads on a 128K prefix: 55 us, 4.9 TB/s). With more, the
+// products of a tile and 64 rows take 64 x 48 cycles, 1.6 us (a product with M = 128 reads
+// 4 KB of A from shared memory, whatever n up to 64), but a tile takes 2.7 us: a part of 32 KB
+// is in the ring of 128 KB for 1.4 us from its copy to the end of its products (16 sequences:
+// 104 us). Small calls are a chain of latencies: two sequences on 100 rows take 11.7 us, 8 on
+// 4096 rows 14.3, of which 3.4 are writing and joining 128 KB of partials a CTA.
 #include <cuda.h>
 #include <math.h>
 
@@ -250,11 +253,11 @@ struct Work {
 };
 
 // ------------------------------------------------------------- shared memory ----
-// A ring stage holds two boxes of 64 keys x 64 columns in fp16, swizzled: a K part is 64
-// columns of a tile's 128 keys (the boxes one below the other are one operand of 128 rows),
-// a V part 64 keys of 128 value dimensions (the boxes are the two halves of M = 128). With
-// parts of twice the size, 128 keys x 128 columns, less of the ring was on its way at a time.
-// int8 rows arrive in a second ring, 128 keys x 128 codes a stage, and are widened.
+// fp16 rows: a ring stage holds a part, 128 keys x 128 columns, as two swizzled blocks of 64
+// columns (V's two are the M = 128 of one product). (Parts of half that size in a ring of 9
+// cost more issues than they saved in waiting: 109 us against 104 on 16 sequences and a 128K
+// prefix.) int8 rows arrive in rings of codes of their own, K's parts whole, V's by halves of
+// 64 keys, and are widened: K into tensor memory, V into this ring.
 template <int HD, bool I8>
 struct Plan {
   static constexpr int kStages = I8 || HD == 512 ? 4 : 5;
@@ -275,6 +278,7 @@ struct Plan {
   static constexpr int kCodes = kRing + kStages * kStage;
   static constexpr int kValues = kCodes + kKeyCodes * kKeyCode;
   static constexpr int kState = kValues + kValueCodes * kValueCode;
+  static_assert(I8 ? kStages % 2 == 0 && kValueCodes % 2 == 0 : HD / 128 <= kStages, "ring sizes");
 };
 
 constexpr int kQueue = 2;  // segments that the scheduling warp is ahead at most
@@ -706,6 +710,12 @@ Q4G_DEV void widen16(uint4 u, uint32_t (&h)[8]) {
   for (int k = 0; k < 4; ++k) h[2 * k] = widen2(w[k], 0x4140), h[2 * k + 1] = widen2(w[k], 0x4342);
 }
 
+// int8 rows take 3.5 us a tile and 64 rows (fp16 rows 2.7): the roles use half of the issue
+// slots and wait for one another. Measured on the way, 64 sequences on a 32K prefix: all parts
+// widened through shared memory's one ring by two groups 149 us, K and V by groups of their
+// own 138, V without selects and by halves 122, two buffers of P^T 121; a second group for K
+// 120 there, but 73 against 70 us for 8 sequences on a 128K prefix.
+//
 // K parts become operand A in tensor memory (a thread is a key).
 template <int HD>
 Q4G_DEV void convert_keys(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh) {

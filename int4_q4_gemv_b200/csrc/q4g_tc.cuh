@@ -72,7 +72,7 @@ Q4G_DEV void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: 
 // True in one lane of a converged warp, always the same. Products, commits and tensor
 // copies issue from a branch on it: the compiler then keeps their descriptors in uniform
 // registers. In a branch on a thread index it takes them lane by lane: 140 cycles per
-// product against 64 to 68 (M = 128, n = 16..64).
+// product against 48 to 73 (M = 128, n = 16..64).
 Q4G_DEV bool elect_one() {
   uint32_t r;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
