@@ -716,6 +716,10 @@ Q4G_DEV void widen16(uint4 u, uint32_t (&h)[8]) {
 // own 138, V without selects and by halves 122, two buffers of P^T 121; a second group for K
 // 120 there, but 73 against 70 us for 8 sequences on a 128K prefix.
 //
+// A stage of codes is given back when what they became is written: every lane has used its
+// loads then. (Given back after the loads, before a wait and their use, the next copy could
+// overwrite codes: wrong values in one block of value dimensions, seldom.)
+//
 // K parts become operand A in tensor memory (a thread is a key).
 template <int HD>
 Q4G_DEV void convert_keys(const SharedParams& p, unsigned char* smem, RingState<HD, true>& sh) {
@@ -738,10 +742,6 @@ Q4G_DEV void convert_keys(const SharedParams& p, unsigned char* smem, RingState<
         uint4 u[4];
 #pragma unroll
         for (int x = 0; x < 4; ++x) u[x] = *reinterpret_cast<const uint4*>(src + (((half * 4 + x) ^ (tid & 7)) * 16));
-        if (half == 1) {  // the codes are in registers: their stage is free
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.kc_empty[rc.at]);
-        }
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
           float v[16];
@@ -755,11 +755,11 @@ Q4G_DEV void convert_keys(const SharedParams& p, unsigned char* smem, RingState<
           tmem_st16(key_lanes + rk.at * kKeyCols + half * 32 + x * 16, v);
         }
       }
-      rc.step();
       tmem_wait_st();
       tc_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.k_full[rk.at]);
+      if (lane == 0) mbar_arrive(&sh.k_full[rk.at]), mbar_arrive(&sh.kc_empty[rc.at]);
+      rc.step();
       rk.step();
     }
   }
@@ -789,8 +789,6 @@ Q4G_DEV void convert_values(const SharedParams& p, unsigned char* smem, RingStat
       uint4 u[4];
 #pragma unroll
       for (int x = 0; x < 4; ++x) u[x] = *reinterpret_cast<const uint4*>(src + x * 2048);
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.vc_empty[rc.at]);
       if (!wait_warp(sh, p, &sh.empty[rv.at], rv.phase)) return;
       unsigned char* const dst = smem + P::kRing + rv.at * P::kStage;
 #pragma unroll
@@ -802,7 +800,7 @@ Q4G_DEV void convert_values(const SharedParams& p, unsigned char* smem, RingStat
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.full[1][rv.at]);
+      if (lane == 0) mbar_arrive(&sh.full[1][rv.at]), mbar_arrive(&sh.vc_empty[rc.at]);
       rc.step(), rc.step();
       rv.step(), rv.step();
     }

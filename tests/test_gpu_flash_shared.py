@@ -128,6 +128,21 @@ def test_many_rows_heads_and_sequences(batch, n_q, n_kv, hd, prefix, cap, i8):
 
 
 @pytest.mark.parametrize("i8", [False, True])
+@pytest.mark.parametrize("batch,n_q,n_kv,hd,prefix,cap", [(130, 128, 2, 512, 1000, 5), (130, 130, 2, 512, 1000, 0),
+                                                          (100, 64, 1, 256, 1500, 300), (256, 96, 3, 256, 700, 40)])
+def test_many_segments_of_many_tiles_per_cta(batch, n_q, n_kv, hd, prefix, cap, i8):
+    """More units than CTAs, each of several tiles: every ring is full of the next segment's
+    rows while one ends. Right, and the same bits each time."""
+    lens = np.random.default_rng(n_q).integers(0, cap + 1, batch).tolist()
+    t = Batch(batch, n_q, n_kv, hd, prefix, cap, lens if cap else [], i8, seed=prefix)
+    first = t.run().clone()
+    t.check()
+    for _ in range(40):
+        t.out.zero_()
+        assert torch.equal(t.run(), first)
+
+
+@pytest.mark.parametrize("i8", [False, True])
 def test_rows_behind_the_length_are_never_used(i8):
     """Own rows from own_len on hold NaN and infinities, and so does what surrounds them."""
     t = Batch(4, 16, 1, 512, 300, 150, [0, 1, 129, 100], i8, seed=3)
