@@ -217,8 +217,9 @@ q4g_status q4g_kv_read_ring_i8(const int8_t* k_codes, const float* k_scales, con
  * [batch][own_capacity][n_kv][hd], of which the first own_len[b] (device int32
  * [batch], clamped into [0, own_capacity]) are attended, the query's own row
  * among them. Sequence b's queries attend all prefix rows and its own rows; query
- * head h uses KV head h / (n_q / n_kv). Scale 1.0, fp32 online softmax, fp16
- * output [batch][n_q][hd]; a sequence without any row (prefix_len 0, own_len 0)
+ * head h uses KV head h / (n_q / n_kv). Scale 1.0, fp32 online softmax, the
+ * probabilities in the product with V as fp16 hi + lo (2^-22 relative), fp16 output
+ * [batch][n_q][hd]; a sequence without any row (prefix_len 0, own_len 0)
  * gives zeros. Own rows from own_len[b] on are never used, whatever they hold.
  * hd must be 256 or 512; 1 <= batch <= 256, n_q <= 1024, 0 <= prefix_len <= 2^30,
  * 0 <= own_capacity <= 2^24, batch * own_capacity <= 2^30 (k_prefix and v_prefix

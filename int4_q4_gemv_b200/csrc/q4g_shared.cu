@@ -14,8 +14,9 @@
 // Softmax: a column (query row) has a reference exponent that the probabilities are
 // taken against, 2^(s log2 e - ref + 7); it is raised, and the sums and O^T rescaled,
 // only when a tile's maximum passes it by 8, so weights stay below 2^15 and rescaling
-// is rare. Probabilities (times the V scale) are rounded to fp16 for the second
-// product, 2^-11 relative as the fp16 output itself; sums and O^T are fp32. With int8
+// is rare. Probabilities (times the V scale) enter the second product as fp16 hi + lo,
+// 2^-22 relative, as in the one-sequence kernels: one fp16 each would put an error of the
+// size of the fp16 output's own rounding on top of it. Sums and O^T are fp32. With int8
 // rows the reference covers the weight p * scale, not p, so no scale overflows fp16.
 //
 // Work: a unit is a row group of a KV head over the prefix, or a sequence's heads over
@@ -29,10 +30,11 @@
 // Bound by HBM for one row group: a 128-key tile of hd 512 is 256 KB, 5.6 us of an SM's
 // share of HBM (4 sequences of 16 heads on a 128K prefix: 55 us, 4.9 TB/s). With more, the
 // products of a tile and 64 rows take 64 x 48 cycles, 1.6 us (a product with M = 128 reads
-// 4 KB of A from shared memory, whatever n up to 64), but a tile takes 2.7 us: a part of 32 KB
-// is in the ring of 128 KB for 1.4 us from its copy to the end of its products (16 sequences:
-// 104 us). Small calls are a chain of latencies: two sequences on 100 rows take 11.7 us, 8 on
-// 4096 rows 14.3, of which 3.4 are writing and joining 128 KB of partials a CTA.
+// 4 KB of A from shared memory, whatever n up to 64) for hi and 32 x 48 more for lo, 2.4 us,
+// and the parts of V stay in the ring of 128 KB that much longer (16 sequences: 132 us; with
+// hi alone 103, and 1.4 times the error of the output's own rounding). Small calls are a chain
+// of latencies: two sequences on 100 rows take 11.4 us, 8 on 4096 rows 15.3, of which 3.4 are
+// writing and joining 128 KB of partials a CTA.
 #include <cuda.h>
 #include <math.h>
 
@@ -265,7 +267,6 @@ struct Plan {
   // codes: stages of K parts and of V parts (those and V's ring stages even: each of the two
   // groups that widen V has its own)
   static constexpr int kKeyCodes = I8 ? (HD == 512 ? 2 : 4) : 0, kValueCodes = I8 ? 4 : 0;
-  static constexpr int kProbs = I8 ? 2 : 1;  // buffers of P^T
   static constexpr int kThreads = 32 * (4 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
   static constexpr int kStage = kTileKeys * 256 / kHalves;  // bytes
   static constexpr int kBox = kStage / 2;                   // a block of 64 columns
@@ -273,8 +274,8 @@ struct Plan {
   static constexpr int kQSlab = kGroupRows * 128;
   static constexpr int kQ = 0;
   static constexpr int kP = kQ + HD / 64 * kQSlab;
-  static constexpr int kPBytes = kTileKeys * 128;
-  static constexpr int kRing = kP + kProbs * kPBytes;
+  static constexpr int kPBytes = kTileKeys * 128;  // P^T: hi, then lo
+  static constexpr int kRing = kP + 2 * kPBytes;
   static constexpr int kCodes = kRing + kStages * kStage;
   static constexpr int kValues = kCodes + kKeyCodes * kKeyCode;
   static constexpr int kState = kValues + kValueCodes * kValueCode;
@@ -290,7 +291,7 @@ struct State {
   float factor[kGroupRows];
   Segment seg[kQueue];
   uint64_t seg_full[kQueue], seg_empty[kQueue];
-  uint64_t s_full[2], s_free[2], p_full[2], pv_done[2], q_full, q_free, o_free, drain[2];
+  uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_free, o_free, drain[2];
   int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
   int32_t clean_at;  // the ring stage of the first V part to clear
@@ -643,8 +644,7 @@ Q4G_DEV void multiply_values(const SharedParams& p, unsigned char* smem, RingSta
     for (int i = 0; i < s.tiles && ok; ++i, ++tile) {
       const bool last = i == s.tiles - 1;
       if (!I8 && !last) r.skip(C);  // the next tile's K parts
-      const int buf = tile % P::kProbs;
-      if (!(ok = wait(sh, p, &sh.p_full[buf], (tile / P::kProbs) & 1))) break;
+      if (!(ok = wait(sh, p, &sh.p_full, tile & 1))) break;
       // the live keys, rounded up to 16
       const int live = min(kTileKeys, s.key_end - s.key0 - i * kTileKeys);
       const int steps = (live + 15) >> 4;
@@ -657,7 +657,6 @@ Q4G_DEV void multiply_values(const SharedParams& p, unsigned char* smem, RingSta
           if (!ok) break;
         }
       }
-      const uint64_t pb = pt + buf * (P::kPBytes >> 4);
 #pragma unroll 1
       for (int c = 0; c < P::kHalves * C; ++c) {
         if (!(ok = wait(sh, p, &sh.full[1][r.at], r.phase()))) break;
@@ -667,22 +666,25 @@ Q4G_DEV void multiply_values(const SharedParams& p, unsigned char* smem, RingSta
           if (last && clean && !(ok = wait(sh, p, &sh.clean_done[d], cleaned & 1))) break;
         }
         tc_fence_after();
-        const uint64_t a = ring + r.at * (P::kStage >> 4), b = pb + half * (kSteps * 128);
+        const uint64_t a = ring + r.at * (P::kStage >> 4), b = pt + half * (kSteps * 128);
         const uint32_t o_at = o_col + d * kGroupRows;
+        auto product = [&](int k) {
+          tc_mma_f16(o_at, a + k * 128, b + k * 128, id, i > 0 || half > 0 || k > 0);
+          tc_mma_f16(o_at, a + k * 128, b + (P::kPBytes >> 4) + k * 128, id, true);
+        };
         if (steps == kTileKeys / 16) {
 #pragma unroll
-          for (int k = 0; k < kSteps; ++k) tc_mma_f16(o_at, a + k * 128, b + k * 128, id, i > 0 || half > 0 || k > 0);
+          for (int k = 0; k < kSteps; ++k) product(k);
         } else {
 #pragma unroll 1
-          for (int k = 0; k < kSteps && half * kSteps + k < steps; ++k)
-            tc_mma_f16(o_at, a + k * 128, b + k * 128, id, i > 0 || half > 0 || k > 0);
+          for (int k = 0; k < kSteps && half * kSteps + k < steps; ++k) product(k);
         }
         tc_commit(&sh.empty[r.at]);
         if (last && half == P::kHalves - 1) tc_commit(&sh.o_part[d]);  // 128 of the value dimensions are complete
         r.step();
       }
       if (!ok) break;
-      tc_commit(&sh.pv_done[buf]);
+      tc_commit(&sh.pv_done);
     }
     if (clean) ++cleaned;
     ++seg;
@@ -710,11 +712,11 @@ Q4G_DEV void widen16(uint4 u, uint32_t (&h)[8]) {
   for (int k = 0; k < 4; ++k) h[2 * k] = widen2(w[k], 0x4140), h[2 * k + 1] = widen2(w[k], 0x4342);
 }
 
-// int8 rows take 3.5 us a tile and 64 rows (fp16 rows 2.7): the roles use half of the issue
-// slots and wait for one another. Measured on the way, 64 sequences on a 32K prefix: all parts
+// int8 rows out of L2 take longer than fp16 rows (64 sequences on a 32K prefix: 144 us against
+// 130): the roles use half of the issue slots and wait for one another. Measured on the way, 64 sequences on a 32K prefix: all parts
 // widened through shared memory's one ring by two groups 149 us, K and V by groups of their
-// own 138, V without selects and by halves 122, two buffers of P^T 121; a second group for K
-// 120 there, but 73 against 70 us for 8 sequences on a 128K prefix.
+// own 138, V without selects and by halves 122; a second group for K 120 there, but 73
+// against 70 us for 8 sequences on a 128K prefix. With lo beside hi in P^T 144 and 80.
 //
 // A stage of codes is given back when what they became is written: every lane has used its
 // loads then. (Given back after the loads, before a wait and their use, the next copy could
@@ -879,11 +881,8 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
         if (j == 0 || raise) sh.ref[tid] = m;
       }
       raise = softmax_any(raise);
-      // P^T's buffer is free; and O^T if it changes here
-      constexpr uint32_t NB = P::kProbs;
-      const uint32_t pb = tile % NB;
-      if (tile >= NB) ok = ok && wait_warp(sh, p, &sh.pv_done[pb], (tile / NB - 1) & 1);
-      if (NB > 1 && raise) ok = ok && wait_warp(sh, p, &sh.pv_done[(tile - 1) % NB], ((tile - 1) / NB) & 1);
+      // P^T's buffer is free, and O^T may change here
+      if (tile > 0) ok = ok && wait_warp(sh, p, &sh.pv_done, (tile - 1) & 1);
       if (active) {
         if (raise) {
           tc_fence_after();
@@ -903,25 +902,31 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
 #pragma unroll
           for (int i = 0; i < 32; ++i) l[i] *= sh.factor[c0 + i];
         }
-        unsigned char* const row = smem + P::kP + pb * P::kPBytes + key * 128;
+        unsigned char* const row = smem + P::kP + key * 128;
 #pragma unroll
         for (int i = 0; i < 32; i += 8) {
-          uint32_t h[4];
+          uint32_t hi[4], lo[4];
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
             const float2 ref = *reinterpret_cast<const float2*>(&sh.ref[c0 + i + e]);
             const float a = ex2(x[i + e] - ref.x + kOffset), b = ex2(x[i + e + 1] - ref.y + kOffset);
             l[i + e] += a;
             l[i + e + 1] += b;
-            const __half2 ab = I8 ? __floats2half2_rn(a * vs, b * vs) : __floats2half2_rn(a, b);
-            h[e / 2] = *reinterpret_cast<const uint32_t*>(&ab);
+            const float u = I8 ? a * vs : a, w = I8 ? b * vs : b;
+            const __half2 h = __floats2half2_rn(u, w);
+            const float2 f = __half22float2(h);
+            const __half2 rest = __floats2half2_rn(u - f.x, w - f.y);
+            hi[e / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            lo[e / 2] = *reinterpret_cast<const uint32_t*>(&rest);
           }
-          *reinterpret_cast<uint4*>(row + ((((c0 + i) >> 3) ^ (key & 7)) * 16)) = make_uint4(h[0], h[1], h[2], h[3]);
+          unsigned char* const at = row + ((((c0 + i) >> 3) ^ (key & 7)) * 16);
+          *reinterpret_cast<uint4*>(at) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+          *reinterpret_cast<uint4*>(at + P::kPBytes) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
         }
       }
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.p_full[pb]);
+      if (lane == 0) mbar_arrive(&sh.p_full);
     }
 
     // the segment's partial, by blocks of 128 value dimensions as they are complete: thread =
@@ -1015,9 +1020,9 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kSoftmaxWarps);
-      mbar_init(&sh.p_full[i], kSoftmaxWarps);
-      mbar_init(&sh.pv_done[i], 1);
     }
+    mbar_init(&sh.p_full, kSoftmaxWarps);
+    mbar_init(&sh.pv_done, 1);
     mbar_init(&sh.q_full, 1);
     mbar_init(&sh.q_free, 1);
     for (int i = 0; i < HD / 128; ++i) mbar_init(&sh.o_part[i], 1);
