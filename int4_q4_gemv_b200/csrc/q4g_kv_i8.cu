@@ -81,6 +81,12 @@ Q4G_DEV void quantize(float (&v)[E], float s, bool no_nan, uint32_t (&w)[E / 4])
   }
 }
 
+// Element offset of (t, h) among the fp16 rows; head counts may pass 2^31 / hd.
+template <int HD>
+Q4G_DEV int64_t row_offset(const KvCopyParams& p, int t, int h) {
+  return t * p.row_stride + (int64_t)h * HD;
+}
+
 constexpr int E = 16;  // values of a row per lane
 template <int HD>
 constexpr int kRowLanes = HD / E;
@@ -114,7 +120,7 @@ __global__ void __launch_bounds__(kKvThreads, 5) kv_write_kernel(const KvCopyPar
     next_row = -1;
     if (i >= total) return;
     const int t = i / p.n_kv, h = i - t * p.n_kv;
-    load_row<HD>(rows + t * p.row_stride + h * HD, next);
+    load_row<HD>(rows + row_offset<HD>(p, t, h), next);
     next_row = cache_row(p, t, h);
   };
   load();
@@ -166,7 +172,7 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCopyParams 
   auto load = [&]() {
     if (i >= total) return;
     const int t = i / p.n_kv, h = i - t * p.n_kv;
-    next_out = rows + t * p.row_stride + h * HD;
+    next_out = rows + row_offset<HD>(p, t, h);
     const int64_t row = cache_row(p, t, h);
     next[0] = next[1] = make_uint2(0u, 0u);  // a slot outside the cache: zeros
     next_s = 0.f;
