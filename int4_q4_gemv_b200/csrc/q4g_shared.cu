@@ -440,6 +440,13 @@ Q4G_DEV bool take(State& sh, const SharedParams& p, uint32_t i, Segment& s) {
   s = sh.seg[i % kQueue];
   return s.tiles > 0;
 }
+// The same for a warp: all lanes agree, and have read the segment before one gives it back
+// (a vote orders no memory, __syncwarp does).
+Q4G_DEV bool take_warp(State& sh, const SharedParams& p, uint32_t i, Segment& s) {
+  const bool more = __all_sync(0xffffffffu, take(sh, p, i, s));
+  __syncwarp();
+  return more;
+}
 Q4G_DEV void give_back(State& sh, uint32_t i) { mbar_arrive(&sh.seg_empty[i % kQueue]); }
 
 // A role's place in a ring of N stages and the phase that its next wait is for.
@@ -731,7 +738,7 @@ Q4G_DEV void convert_keys(const SharedParams& p, unsigned char* smem, RingState<
   Ring<P::kKeyCodes> rc(0);
   Ring<2> rk(1);
   Segment s;
-  for (uint32_t seg = 0; __all_sync(0xffffffffu, take(sh, p, seg, s)); ++seg) {
+  for (uint32_t seg = 0; take_warp(sh, p, seg, s); ++seg) {
     if (lane == 0) give_back(sh, seg);
 #pragma unroll 1
     for (int c = 0; c < s.tiles * (HD / 128); ++c) {
@@ -782,7 +789,7 @@ Q4G_DEV void convert_values(const SharedParams& p, unsigned char* smem, RingStat
   Ring<P::kStages> rv(1);
   Segment s;
   if (group == 1) rc.step(), rv.step();
-  for (uint32_t seg = 0; __all_sync(0xffffffffu, take(sh, p, seg, s)); ++seg) {
+  for (uint32_t seg = 0; take_warp(sh, p, seg, s); ++seg) {
     if (lane == 0) give_back(sh, seg);
 #pragma unroll 1
     for (int c = 0; c < s.tiles * (HD / 128); ++c) {
