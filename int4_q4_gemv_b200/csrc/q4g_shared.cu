@@ -945,10 +945,11 @@ Q4G_DEV void softmax(const SharedParams& p, unsigned char* smem, RingState<HD, I
         const int from = s.key_end & (kTileKeys - 1), chunks = (16 - (from & 15)) * 16;  // of both boxes
         for (int c = 0; c < C; ++c) {
           ok = ok && wait_warp(sh, p, &sh.clean_ask[c], cleaned & 1);
-          const int at = (sh.clean_at + c) % P::kStages;
-          if (tid < chunks)
+          if (ok && tid < chunks) {  // (given up: clean_at may hold anything)
+            const int at = (sh.clean_at + c) % P::kStages;
             *reinterpret_cast<uint4*>(smem + P::kRing + at * P::kStage + (tid & 1) * P::kBox + from * 128 + (tid >> 1) * 16) =
                 make_uint4(0, 0, 0, 0);
+          }
           fence_async_smem();
           __syncwarp();
           if (lane == 0) mbar_arrive(&sh.clean_done[c]);
