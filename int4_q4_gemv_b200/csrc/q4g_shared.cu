@@ -294,6 +294,7 @@ struct State {
   uint64_t s_full[2], s_free[2], p_full, pv_done, q_full, q_free, o_free, drain[2];
   int32_t own_places[kMaxBatch + 1];
   uint32_t tmem;
+  uint32_t fills, last, items;  // of the copying thread, at its end
   int32_t clean_at;  // the ring stage of the first V part to clear
   volatile int abort;
 };
@@ -538,17 +539,23 @@ Q4G_DEV void produce(const SharedParams& p, const SharedMaps& maps, unsigned cha
       }
     }
   }
-  // Given up: the copies in flight still write this CTA's shared memory. Each is the last of
-  // its stage (and, of a stage with one barrier for K and one for V, kind), so its phase stays.
-  if (!ok || sh.abort) {
-    if constexpr (I8) {  // a stage that was never filled has no phase to wait for: that wait is over at once
-      for (int k = 0; k < NK; ++k) mbar_wait_bounded(&sh.kc_full[k], ((fills >> k) & 1) ^ 1, 20000000ull);
-      for (int k = 0; k < NV; ++k) mbar_wait_bounded(&sh.vc_full[k], ((fills >> (16 + k)) & 1) ^ 1, 20000000ull);
-    } else {
-      for (int k = 0; k < NK && k < (int)items; ++k) {
-        const int kind = (last >> k) & 1;
-        mbar_wait_bounded((kind ? sh.full[1] : sh.full[0]) + k, ((fills >> (16 * kind + k)) & 1) ^ 1, 20000000ull);
-      }
+  sh.fills = fills, sh.last = last, sh.items = items;
+}
+
+// After a wait has given up and every role has ended: copies in flight still write this CTA's
+// shared memory. Each is the last of its stage (and, of a stage with one barrier for K and one
+// for V, kind), so its phase stays. (The queries' are waited for where they are made.)
+template <int HD, bool I8>
+Q4G_DEV void drain_copies(const SharedParams& p, RingState<HD, I8>& sh) {
+  using P = Plan<HD, I8>;
+  const uint32_t fills = sh.fills;
+  if constexpr (I8) {  // a stage that was never filled has no phase to wait for: that wait is over at once
+    for (int k = 0; k < P::kKeyCodes; ++k) mbar_wait_bounded(&sh.kc_full[k], ((fills >> k) & 1) ^ 1, p.wait_ns);
+    for (int k = 0; k < P::kValueCodes; ++k) mbar_wait_bounded(&sh.vc_full[k], ((fills >> (16 + k)) & 1) ^ 1, p.wait_ns);
+  } else {
+    for (int k = 0; k < P::kStages && k < (int)sh.items; ++k) {
+      const int kind = (sh.last >> k) & 1;
+      mbar_wait_bounded((kind ? sh.full[1] : sh.full[0]) + k, ((fills >> (16 * kind + k)) & 1) ^ 1, p.wait_ns);
     }
   }
 }
@@ -585,7 +592,7 @@ Q4G_DEV void multiply_keys(const SharedParams& p, const SharedMaps& maps, unsign
     for (int c = 0; c < HD / 64; ++c)
       tma_load_4d(smem + P::kQ + c * P::kQSlab, s.own ? &maps.own_q : &maps.q, c * 64, s.g0, s.h, s.b, &sh.q_full);
     if (!(ok = wait(sh, p, &sh.q_full, seg & 1))) {
-      mbar_wait_bounded(&sh.q_full, seg & 1, 20000000ull);  // the copies write this CTA's shared memory
+      mbar_wait_bounded(&sh.q_full, seg & 1, p.wait_ns);  // the copies write this CTA's shared memory
       break;
     }
     for (int i = 0; i < s.tiles && ok; ++i, ++tile) {
@@ -624,10 +631,6 @@ Q4G_DEV void multiply_keys(const SharedParams& p, const SharedMaps& maps, unsign
       }
     }
     ++seg;
-  }
-  if (!ok || sh.abort) {  // given up: products in flight still use shared and tensor memory
-    tc_commit(&sh.drain[0]);
-    mbar_wait_bounded(&sh.drain[0], 0, p.wait_ns);
   }
 }
 
@@ -695,10 +698,6 @@ Q4G_DEV void multiply_values(const SharedParams& p, unsigned char* smem, RingSta
     }
     if (clean) ++cleaned;
     ++seg;
-  }
-  if (!ok || sh.abort) {  // as above
-    tc_commit(&sh.drain[1]);
-    mbar_wait_bounded(&sh.drain[1], 0, p.wait_ns);
   }
 }
 
@@ -1076,6 +1075,19 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   }
   tc_fence_before();
   __syncthreads();
+  if (sh.abort) {  // no role issues any more, but copies and products in flight use shared and tensor memory
+    if (warp == 0) {
+      if (elect_one()) drain_copies<HD, I8>(p, sh);
+      __syncwarp();
+    } else if (warp <= 2) {
+      if (elect_one()) {  // the thread that made the products
+        tc_commit(&sh.drain[warp - 1]);
+        mbar_wait_bounded(&sh.drain[warp - 1], 0, p.wait_ns);
+      }
+      __syncwarp();
+    }
+    __syncthreads();
+  }
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(sh.tmem, 512);
