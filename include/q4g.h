@@ -226,9 +226,13 @@ q4g_status q4g_kv_read_ring_i8(const int8_t* k_codes, const float* k_scales, con
  * may be NULL if prefix_len is 0; k_own, v_own and own_len if own_capacity is 0).
  * workspace: device buffer of q4g_flash_decode_shared_workspace_bytes(batch, n_q,
  * n_kv, hd) bytes, 256-byte aligned, used as scratch by this call (calls that
- * share a workspace must not overlap on the GPU). Every wait inside the kernel is
- * limited in time; one that gives up sets the error word that q4g_model_check
- * reports. */
+ * share a workspace must not overlap on the GPU). Waits on a barrier in memory are
+ * limited: 2 s each, 60 s in the warp that hands out work, and after a give-up 2 s
+ * each for the copies and products in flight. One that gives up sets the error word
+ * that q4g_model_check reports (with or without a model); the call has returned
+ * Q4G_OK by then, and its output is unspecified. No limit have the hardware's own
+ * waits, for tensor memory that another kernel on the SM holds and between the warps
+ * of a softmax, which all reach the same barriers. */
 size_t q4g_flash_decode_shared_workspace_bytes(int32_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim);
 q4g_status q4g_flash_decode_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_kv, int32_t head_dim,
                                    const uint16_t* k_prefix, const uint16_t* v_prefix, int64_t prefix_len,
@@ -374,8 +378,10 @@ q4g_status q4g_model_create(const q4g_config* cfg, const q4g_weights* w, q4g_mod
 void q4g_model_destroy(q4g_model* m);
 
 /* Reports (and clears) the device-side error word that a bounded wait sets when
- * it gives up (Q4G_ETIMEOUT; every wait inside the kernels is limited in time,
- * 2 s by default) and any sticky CUDA error (Q4G_ECUDA). Synchronises `stream`.
+ * it gives up (Q4G_ETIMEOUT; waits inside the kernels are limited in time, 2 s by
+ * default) and any sticky CUDA error (Q4G_ECUDA). Synchronises `stream`. There is one
+ * word per device, the current one's is read: m may be NULL, for a program that calls
+ * the standalone entry points without a model.
  * Diagnostics: with Q4G_DEBUG_SYNC set in the environment, eager (non-graph)
  * steps synchronise after every launch and name the launch that failed. */
 q4g_status q4g_model_check(q4g_model* m, q4g_stream_t stream);
@@ -393,7 +399,12 @@ typedef enum {
                                  stage of the first GEMV expects 16 bytes that never
                                  arrive; its bounded wait (20 ms) gives up, the step
                                  finishes with unspecified results and
-                                 q4g_model_check returns Q4G_ETIMEOUT. One-shot. */
+                                 q4g_model_check returns Q4G_ETIMEOUT. One-shot.
+                                 With m NULL: the same for the calling thread's next
+                                 q4g_flash_decode_shared or _i8, where a barrier of the
+                                 first CTA never completes: 1 keys, 2 values, 3 queries,
+                                 4 probabilities, 5 the handing out of work (which takes
+                                 more than two units of work for that CTA) */
   Q4G_OPT_ATTN_CLUSTER = 6, /* [1] sliding layers: the 8 key chunks of a KV head run
                                  as one thread-block cluster and merge their partial
                                  softmax sums through distributed shared memory;

@@ -341,8 +341,7 @@ extern "C" void q4g_model_destroy(q4g_model* m) {
   delete m;
 }
 
-extern "C" q4g_status q4g_model_check(q4g_model* m, q4g_stream_t stream) {
-  if (!m) return fail(Q4G_EINVAL, "model is NULL");
+extern "C" q4g_status q4g_model_check(q4g_model*, q4g_stream_t stream) {  // the word is the device's, not a model's
   CK(cudaStreamSynchronize((cudaStream_t)stream));
   CK(cudaGetLastError());
   int32_t* ew = device_error_word();
@@ -352,13 +351,20 @@ extern "C" q4g_status q4g_model_check(q4g_model* m, q4g_stream_t stream) {
   if (word) {
     const int32_t zero = 0;
     CK(cudaMemcpy(ew, &zero, sizeof zero, cudaMemcpyHostToDevice));
-    return fail(Q4G_ETIMEOUT, "a bounded device wait gave up (error word 0x%x); results of that step are unspecified",
+    return fail(Q4G_ETIMEOUT, "a bounded device wait gave up in %s (error word 0x%x); its results are unspecified",
+                word == kErrShared ? "a shared-prefix attention call"
+                : word & kErrShared ? "a decode step or GEMV and in a shared-prefix attention call" : "a decode step or GEMV",
                 word);
   }
   return Q4G_OK;
 }
 
 extern "C" q4g_status q4g_model_set_option(q4g_model* m, q4g_option opt, intptr_t value) {
+  if (!m && opt == Q4G_OPT_TEST_STALL) {
+    if (value < 0 || value > kSharedStalls) return fail(Q4G_EINVAL, "stall outside [0, %d]", kSharedStalls);
+    set_shared_stall((int)value);
+    return Q4G_OK;
+  }
   if (!m) return fail(Q4G_EINVAL, "model is NULL");
   std::lock_guard<std::mutex> lk(m->mu);
   switch (opt) {

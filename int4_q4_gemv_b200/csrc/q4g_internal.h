@@ -87,8 +87,15 @@ bool set_gemv_kernel_choice(int kind);
 constexpr int kGemvTraceSlots = 256;
 constexpr int kPrefillChunk = 64;  // rows of one prefill call
 constexpr int kPrefillBlock = 4;   // rows per pass inside a prefill call  // one GEMV launch's timeline (GemvParams::trace)
-// Device address of the library's error word (bit 0: a bounded wait gave up).
+// Device address of the library's error word: a bounded wait gave up in a GEMV (bit 0) or
+// in shared-prefix attention (bit 1).
+constexpr int32_t kErrShared = 2;
 int32_t* device_error_word();
+// Test: a barrier of CTA 0 of the thread's next shared-prefix attention call waits for an
+// arrival that never comes, with a limit of 20 ms. 1: a part of K, 2: of V, 3: the queries,
+// 4: probabilities, 5: room for a third segment; 0: none.
+constexpr int kSharedStalls = 5;
+void set_shared_stall(int kind);
 
 // ------------------------------------------------------------ attention ----
 struct AttnParams {

@@ -80,6 +80,7 @@ struct SharedParams {
   __half* out;
   int32_t* err;
   uint64_t wait_ns;
+  int32_t stall;  // test (set_shared_stall)
 };
 
 struct alignas(64) SharedMaps {
@@ -337,7 +338,7 @@ Q4G_DEV bool wait(State& sh, const SharedParams& p, uint64_t* bar, uint32_t phas
     if (global_ns() - t0 > p.wait_ns) break;
   }
   sh.abort = 1;
-  atomicOr(p.err, 1);
+  atomicOr(p.err, kErrShared);
   return false;
 }
 // The same for a warp: all lanes agree.
@@ -405,7 +406,7 @@ struct Scheduler {
       room = __all_sync(0xffffffffu, mbar_wait_bounded(&sh.seg_empty[n % kQueue], (n / kQueue - 1) & 1, p.wait_ns));
     if (!room) {
       sh.abort = 1;
-      if (lane == 0) atomicOr(p.err, 1);
+      if (lane == 0) atomicOr(p.err, kErrShared);
       return false;
     }
     if (lane == 0) {
@@ -996,9 +997,11 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   if (warp == 1) {
     tmem_alloc(&sh.tmem, 512);  // at once: with 227 KB of shared memory the CTA is alone on its SM
   } else if (warp == 2 && lane == 0) {
+    // of a stalled ring only the third stage, so that others are in flight
+    const int stall = blockIdx.x == 0 ? p.stall : 0;
     for (int i = 0; i < P::kStages; ++i) {
-      mbar_init(&sh.full[0][i], 1);
-      mbar_init(&sh.full[1][i], I8 ? kGroup / 32 : 1);
+      mbar_init(&sh.full[0][i], 1 + (!I8 && stall == 1 && i == 2));
+      mbar_init(&sh.full[1][i], I8 ? kGroup / 32 : 1 + (stall == 2 && i == 2));
       mbar_init(&sh.empty[i], 1);
     }
     if constexpr (I8) {
@@ -1007,11 +1010,11 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
         mbar_init(&sh.k_empty[i], 1);
       }
       for (int i = 0; i < P::kKeyCodes; ++i) {
-        mbar_init(&sh.kc_full[i], 1);
+        mbar_init(&sh.kc_full[i], 1 + (stall == 1 && i == P::kKeyCodes - 1));
         mbar_init(&sh.kc_empty[i], kGroup / 32);
       }
       for (int i = 0; i < P::kValueCodes; ++i) {
-        mbar_init(&sh.vc_full[i], 1);
+        mbar_init(&sh.vc_full[i], 1 + (stall == 2 && i == 2));
         mbar_init(&sh.vc_empty[i], kGroup / 32);
       }
     } else {
@@ -1022,15 +1025,15 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
     }
     for (int i = 0; i < kQueue; ++i) {
       mbar_init(&sh.seg_full[i], 1);
-      mbar_init(&sh.seg_empty[i], 3 + kSoftmaxWarps + (I8 ? kConvertWarps : 0));
+      mbar_init(&sh.seg_empty[i], 3 + kSoftmaxWarps + (I8 ? kConvertWarps : 0) + (stall == 5));
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 1);
       mbar_init(&sh.s_free[i], kSoftmaxWarps);
     }
-    mbar_init(&sh.p_full, kSoftmaxWarps);
+    mbar_init(&sh.p_full, kSoftmaxWarps + (stall == 4));
     mbar_init(&sh.pv_done, 1);
-    mbar_init(&sh.q_full, 1);
+    mbar_init(&sh.q_full, 1 + (stall == 3));
     mbar_init(&sh.q_free, 1);
     for (int i = 0; i < HD / 128; ++i) mbar_init(&sh.o_part[i], 1);
     mbar_init(&sh.o_free, kSoftmaxWarps);
@@ -1260,6 +1263,7 @@ bool encode_rows(CUtensorMap* m, const void* base, bool i8, int hd, int n_kv, in
 }
 
 constexpr int kMaxDevices = 64;
+thread_local int stall_next = 0;  // set_shared_stall
 
 template <int HD, int kJoinParts>
 cudaError_t launch_join(const SharedParams& p, cudaStream_t st) {
@@ -1390,7 +1394,9 @@ q4g_status run_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_k
   p.own_cap = (int32_t)own_cap;
   p.own_len = own_len;
   p.out = reinterpret_cast<__half*>(out);
-  p.wait_ns = 2000000000ull;
+  p.stall = stall_next;
+  stall_next = 0;
+  p.wait_ns = p.stall ? 20000000ull : 2000000000ull;
   if (!(p.err = device_error_word())) return bad(Q4G_ECUDA, "error word unavailable");
   SharedMaps maps{};
   // queries as [batch][n_kv][G][hd]: a box is the rows of a unit
@@ -1413,6 +1419,8 @@ q4g_status run_shared(const uint16_t* q, int32_t batch, int32_t n_q, int32_t n_k
 }
 
 }  // namespace
+
+void q4g::set_shared_stall(int kind) { stall_next = kind; }
 
 extern "C" size_t q4g_flash_decode_shared_workspace_bytes(int32_t batch, int32_t n_q, int32_t n_kv,
                                                           int32_t head_dim) {

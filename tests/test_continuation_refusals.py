@@ -122,3 +122,11 @@ def test_binding_limit_matches_the_header():
     import re
     text = open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "q4g.h")).read()
     assert int(re.search(r"#define Q4G_LOGPROBS_MAX_TOP (\d+)", text).group(1)) == Q.Q4G_LOGPROBS_MAX_TOP
+
+
+def test_stalls_without_a_model_refused():
+    for opt, value in ((Q.Q4G_OPT_TEST_STALL, -1), (Q.Q4G_OPT_TEST_STALL, 6), (Q.Q4G_OPT_PDL, 1)):
+        with pytest.raises(Q.Q4GError) as e:
+            Q.q4g_model_set_option(0, opt, value)
+        assert e.value.status == EINVAL
+    Q.q4g_model_set_option(0, Q.Q4G_OPT_TEST_STALL, 0)  # none
