@@ -31,11 +31,12 @@ Q4G_DEV uint4 ld_stream_u4(const void* p) {
   return r;
 }
 
-// The same for what the kernel before may have written: volatile, so that it stays behind
-// pdl_wait() (the compiler may move the form above, and __ldg, ahead of it).
+// The same for what the kernel before may have written. Volatile, so that it stays behind
+// pdl_wait() (the compiler may move the form above, and __ldg, ahead of it); and not .nc, which
+// is for data that nobody writes while this kernel exists: it may start before that one ends.
 Q4G_DEV uint4 ld_stream_u4_ordered(const void* p) {
   uint4 r;
-  asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
                : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
                : "l"(p));
   return r;
