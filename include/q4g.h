@@ -211,8 +211,10 @@ q4g_status q4g_kv_read_ring_i8(const int8_t* k_codes, const float* k_scales, con
                                int64_t n_rows, uint16_t* k, uint16_t* v, int64_t row_stride, q4g_stream_t stream);
 
 /* Flash-decode of a batch whose sequences share a prefix (several continuations,
- * or several drafts, of one prompt): every prefix row is read once for the whole
- * batch. q [batch][n_q][hd] fp16, one query per sequence; prefix K/V
+ * or several drafts, of one prompt): every prefix row is read once per 64 query rows
+ * of its KV head, in place of once per sequence. There is no window: a layer whose
+ * queries see W positions may call it while prefix_len and own_len[b] together are at
+ * most W, a full layer always. q [batch][n_q][hd] fp16, one query per sequence; prefix K/V
  * [prefix_len][n_kv][hd]; each sequence's own rows K/V
  * [batch][own_capacity][n_kv][hd], of which the first own_len[b] (device int32
  * [batch], clamped into [0, own_capacity]) are attended, the query's own row
@@ -268,7 +270,7 @@ q4g_status q4g_flash_decode_shared_i8(const uint16_t* q, int32_t batch, int32_t 
  * top_ids and top_logprobs if n_top is 0 (either may be NULL otherwise, not both).
  * 0 <= rows <= 2^20, 1 <= vocab <= 2^30, 0 <= n_top <= min(32, vocab), temperature
  * finite, > 0 and not subnormal. fp32 sums; the same bits on every call.
- * Asynchronous, no scratch memory, one launch. */
+ * Asynchronous, no scratch memory, one launch per 65,535 rows. */
 #define Q4G_LOGPROBS_MAX_TOP 32
 q4g_status q4g_token_logprobs(const float* logits, int64_t rows, int64_t vocab, int64_t row_stride,
                               float temperature, const int32_t* targets, float* logprob, float* entropy,

@@ -1049,7 +1049,9 @@ __global__ void __launch_bounds__(Plan<HD, I8>::kThreads, 1)
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  pdl_launch_dependents();  // the join's CTAs take the places that CTAs of this grid leave
+  // The join's CTAs take the places that CTAs of this grid leave. Not before pdl_wait(): the
+  // join reads own_len ahead of its own wait, and what this grid waited for has written it.
+  pdl_launch_dependents();
   // With int8 rows 768 threads start with 80 registers each: the softmax warps take 120,
   // (64 + 2 x 120 + 3 x 56) x 128 = 472 x 128 of 480 x 128.
   if (warp < 4) {
@@ -1158,7 +1160,7 @@ __global__ void __launch_bounds__(32 * kJoinParts) shared_join_kernel(const Shar
   float2 ml[kJoinMax / kJoinThreads];
   float R = -INFINITY;
   pdl_launch_dependents();
-  pdl_wait();  // all above comes from the call's own arguments
+  pdl_wait();  // all above comes from the arguments and own_len, which is older than shared_kernel's trigger
 #pragma unroll
   for (int k = 0; k < kEarly; ++k)
     if (warp + k * kJoinParts < n) early[k] = o_at(warp + k * kJoinParts);
