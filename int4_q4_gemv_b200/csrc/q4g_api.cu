@@ -41,8 +41,6 @@ q4g_status cuda_fail(cudaError_t e, const char* where) {
     if (e_ != cudaSuccess) return cuda_fail(e_, #expr);  \
   } while (0)
 
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 // qkv column count of a layer type
 struct LayerShape {
   int hd, nkv, nq_cols, k_cols, v_cols, qkv_cols, G, rope_pairs;

@@ -253,6 +253,13 @@ Q4G_DEV void kv_quantize_row_warp(const __half* x, int8_t* codes, float* scale, 
   if (lane == 0) *scale = s;
 }
 
+// 2^x by the hardware's instruction: 2^-22 relative, results below 2^-126 are 0.
+Q4G_DEV float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
 // Block-wide sum for blockDim.x == NT; `red` holds >= 32 floats. All threads
 // receive the result. Summation order is fixed.
 template <int NT = kThreads>

@@ -5,6 +5,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "../../include/q4g.h"
+
 namespace q4g {
 
 // ----------------------------------------------------------------- GEMV ----
@@ -241,5 +243,11 @@ cudaError_t launch_logprobs(const LogprobParams& p, cudaStream_t st);
 
 // Sets the message q4g_last_error() returns on this thread.
 void set_last_error(const char* msg);
+// The refusal of an argument: its status, with the message set.
+inline q4g_status bad(q4g_status s, const char* msg) {
+  set_last_error(msg);
+  return s;
+}
+inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 }  // namespace q4g

@@ -203,13 +203,6 @@ __global__ void __launch_bounds__(kKvThreads) kv_read_kernel(const KvCopyParams 
   }
 }
 
-q4g_status bad(q4g_status s, const char* msg) {
-  set_last_error(msg);
-  return s;
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 // Sizes that the four entry points check alike.
 q4g_status check_sizes(int64_t n_rows, int64_t row_stride, int32_t n_kv, int32_t hd, int64_t capacity) {
   if (hd != 256 && hd != 512) return bad(Q4G_EINVAL, "head_dim must be 256 or 512");

@@ -89,12 +89,6 @@ Q4G_DEV K merge_lists(K a, K b, int lane) {
   return bitonic_merge_desc(a > r ? a : r, lane);
 }
 
-Q4G_DEV float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-
 // Running statistics in base 2: m, l = sum 2^(c (x - m)), e = sum 2^(c (x - m)) c (x - m),
 // with c = log2(e) / T. m starts at the lowest finite value, so a row of -inf keeps l = 0.
 struct Stat {
@@ -399,13 +393,6 @@ __global__ void __launch_bounds__(THREADS, THREADS == kSmall ? 4 : 1) logprob_ke
       p.top_logprobs[at] = (k ? key_value(k) - all.m : __uint_as_float(0x7fc00000u)) / p.temperature - ln;
   }
 }
-
-q4g_status bad(q4g_status s, const char* msg) {
-  set_last_error(msg);
-  return s;
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
 
 template <int THREADS>
 cudaError_t launch_rows(const LogprobParams& p, int ranks, cudaStream_t st) {

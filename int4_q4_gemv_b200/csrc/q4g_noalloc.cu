@@ -44,12 +44,9 @@ cudaError_t scratch_address(void** out) {
   return cudaSuccess;
 }
 
-bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
+using q4g::bad;
 
-q4g_status bad(q4g_status s, const char* msg) {
-  q4g::set_last_error(msg);
-  return s;
-}
+bool aligned16(const void* p) { return ((uintptr_t)p & 15) == 0; }
 
 }  // namespace
 

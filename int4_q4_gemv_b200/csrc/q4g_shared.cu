@@ -362,11 +362,6 @@ Q4G_DEV float warp_max_f32(float v) {
   asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(r) : "f"(v));
   return r;
 }
-Q4G_DEV float ex2(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
 
 // Lane i's result is the sum of v[i] over the warp's lanes: halves change places with
 // the lane 16, 8, ... away, 31 shuffles in place of 160.
@@ -1216,13 +1211,6 @@ __global__ void __launch_bounds__(32 * kJoinParts) shared_join_kernel(const Shar
 }
 
 // -------------------------------------------------------------------- host ----
-q4g_status bad(q4g_status s, const char* msg) {
-  set_last_error(msg);
-  return s;
-}
-
-bool aligned(const void* p, size_t a) { return ((uintptr_t)p % a) == 0; }
-
 typedef CUresult (*EncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
                                 const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
