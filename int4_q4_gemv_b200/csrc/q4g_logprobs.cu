@@ -14,6 +14,9 @@
 // rate) 42 to 44 us without alternatives, 50 to 52 us with 20; tried instead: shares of
 // whole threads (42 MB read again) 60 us, lists kept up to date while reading 98 (a CTA's)
 // and 106 us (a warp's), bulk copies into a ring in shared memory 55 without alternatives.
+// Where the n_top-th largest is no threshold the row is read again in full, through the warps'
+// lists: 256 rows of equal logits take 472 us, with 5 finite logits and n_top 20 655 us (one
+// row 109 and 151, against 9.7).
 // A row is split over the CTAs of one thread-block cluster when there are few rows; they
 // join through distributed shared memory, in rank order, without scratch memory or atomics
 // between CTAs. The sums depend on no timing; candidates arrive in any order, and sorting
@@ -411,7 +414,9 @@ cudaError_t q4g::launch_logprobs(const LogprobParams& p, cudaStream_t st) {
   // in flight within a few tiles (three quarters of the SMs: more clusters do not fit on the
   // GPU at once, 16 rows as 16 clusters of 8 took 22 us, as clusters of 4 they take 12). Many:
   // CTAs of 256 threads, four on every SM at most, the number that fits: one wave, 42 us for
-  // 256 rows of 262,144 logits against 47 with up to six.
+  // 256 rows of 262,144 logits against 47 with up to six. The edges of that rule, rows of 32,003:
+  // 296 rows with two CTAs each 8.6 us, 297 with one 8.9 (with 8 alternatives 13.0 and 12.3);
+  // 592 rows, one wave, 12.0, 600 rows 14.2 (15.4 and 19.7).
   const int sms = device_sm_count();
   const bool large = (int64_t)p.rows * kMaxCluster <= sms && p.vocab > 2 * tile_of(kSmall);
   const int64_t tiles = ((int64_t)p.vocab + tile_of(large ? kLarge : kSmall) - 1) / tile_of(large ? kLarge : kSmall);

@@ -28,13 +28,14 @@
 // partial (reference, sum, O), and a second kernel joins each row's partials.
 //
 // Bound by HBM for one row group: a 128-key tile of hd 512 is 256 KB, 5.6 us of an SM's
-// share of HBM (4 sequences of 16 heads on a 128K prefix: 55 us, 4.9 TB/s). With more, the
+// share of HBM (4 sequences of 16 heads on a 128K prefix: 56 us, 4.8 TB/s). With more, the
 // products of a tile and 64 rows take 64 x 48 cycles, 1.6 us (a product with M = 128 reads
 // 4 KB of A from shared memory, whatever n up to 64) for hi and 32 x 48 more for lo, 2.4 us,
-// and the parts of V stay in the ring of 128 KB that much longer (16 sequences: 132 us; with
-// hi alone 103, and 1.4 times the error of the output's own rounding). Small calls are a chain
-// of latencies: two sequences on 100 rows take 11.4 us, 8 on 4096 rows 15.3, of which 3.4 are
-// writing and joining 128 KB of partials a CTA.
+// and the parts of V stay in the ring of 128 KB that much longer: a tile takes 4.1 us (16
+// sequences: 131 us, or 158 at the 1.6 GHz that the power limit leaves to a run of seconds;
+// with hi alone 103 and 126, at 1.4 times the error of the output's own rounding). Small calls
+// are a chain of latencies: two sequences on 100 rows take 11.4 us, 8 on 4096 rows 15.2, of
+// which about 3.4 are writing and joining 128 KB of partials a CTA.
 #include <cuda.h>
 #include <math.h>
 
@@ -258,9 +259,9 @@ struct Work {
 // ------------------------------------------------------------- shared memory ----
 // fp16 rows: a ring stage holds a part, 128 keys x 128 columns, as two swizzled blocks of 64
 // columns (V's two are the M = 128 of one product). (Parts of half that size in a ring of 9
-// cost more issues than they saved in waiting: 109 us against 104 on 16 sequences and a 128K
-// prefix.) int8 rows arrive in rings of codes of their own, K's parts whole, V's by halves of
-// 64 keys, and are widened: K into tensor memory, V into this ring.
+// cost more issues than they saved in waiting: with hi alone 109 us against 104 on 16 sequences
+// and a 128K prefix.) int8 rows arrive in rings of codes of their own, K's parts whole, V's by
+// halves of 64 keys, and are widened: K into tensor memory, V into this ring.
 template <int HD, bool I8>
 struct Plan {
   static constexpr int kStages = I8 || HD == 512 ? 4 : 5;
