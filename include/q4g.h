@@ -222,7 +222,8 @@ q4g_status q4g_kv_read_ring_i8(const int8_t* k_codes, const float* k_scales, con
  * head h uses KV head h / (n_q / n_kv). Scale 1.0, fp32 online softmax, the
  * probabilities in the product with V as fp16 hi + lo (2^-22 relative), fp16 output
  * [batch][n_q][hd]; a sequence without any row (prefix_len 0, own_len 0)
- * gives zeros. Own rows from own_len[b] on are never used, whatever they hold.
+ * gives zeros. Own rows from own_len[b] on are never used, whatever they hold. An
+ * infinite value in a V row that is attended gives a NaN or an infinity there.
  * hd must be 256 or 512; 1 <= batch <= 256, n_q <= 1024, 0 <= prefix_len <= 2^30,
  * 0 <= own_capacity <= 2^24, batch * own_capacity <= 2^30 (k_prefix and v_prefix
  * may be NULL if prefix_len is 0; k_own, v_own and own_len if own_capacity is 0).
